@@ -26,6 +26,12 @@
  *     in the state.
  *   - Supported sizes: 32 <= M <= 256 with M a power of two, 1 <= K <= M, 1 <= Dv <= 256 with
  *     Dv % 4 == 0. Other sizes return RSM_ERR_UNSUPPORTED.
+ *
+ * Beside the mixer stand the other operators of a hybrid stack, in which attention layers alternate
+ * with mixer layers (Raven README "Model Structure": optional standard attention layers at specified
+ * indices; paperlayer.ai summary section A.6: full or sliding-window attention interleaved,
+ * norms, output gating and skip connections around every block): rsm_window_* (prompts and training),
+ * rsm_paged_* (serving) and rsm_block_norm_*.
  */
 #ifndef RSM_H_
 #define RSM_H_
@@ -50,7 +56,8 @@ typedef enum rsm_status {
   RSM_ERR_CUDA = 3,         /* a CUDA call or launch failed; see rsm_last_error() */
   RSM_ERR_NONFINITE = 4,    /* RSM_FLAG_VALIDATE found a non-finite logit or a non-finite/positive f */
   RSM_ERR_WORKSPACE = 5,    /* workspace missing or smaller than rsm_forward_workspace_size() */
-  RSM_ERR_TIMEOUT = 6       /* a bounded device wait gave up (reported by rsm_get_device_status) */
+  RSM_ERR_TIMEOUT = 6,      /* a bounded device wait gave up (reported by rsm_get_device_status) */
+  RSM_ERR_BAD_PAGE = 7      /* a page table or length outside the cache (reported by rsm_get_device_status) */
 } rsm_status;
 
 typedef enum rsm_dtype { RSM_F32 = 0, RSM_BF16 = 1 } rsm_dtype;
@@ -273,6 +280,211 @@ typedef struct rsm_backward_args {
 RSM_API size_t rsm_backward_workspace_size(const rsm_backward_args* args);
 RSM_API rsm_status rsm_backward(const rsm_backward_args* args, void* stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * rsm_window_forward -- causal attention over a sliding window whose first tokens stay visible.
+ *   Query i sees key j when j <= i and (i - j < window or j < sinks); a window of at least T is
+ *   plain causal attention. With G = H / Hkv, query head h reads key/value head h / G.
+ *     s_ij = scale q_i.k_j over the keys seen, lse_i = log sum_j e^{s_ij},
+ *     o_i = sum_j e^{s_ij - lse_i} v_j
+ *   q       [B,T,H,D] in dtype;  k, v [B,T,Hkv,D] in dtype
+ *   o       [B,T,H,D] in dtype (required)
+ *   lse     [B,T,H] fp32, or NULL to skip: natural logarithm of the row's sum (the backward reads it)
+ *   Scores, softmax statistics and sums are fp32. With bf16 inputs the softmax weights are rounded
+ *   to bf16 for the product with v; with fp32 inputs everything is fp32.
+ *   q, k and v must be finite (checked when RSM_FLAG_VALIDATE is set): a weight of zero does not
+ *   hide an infinity in v.
+ *   Supported: 8 <= D <= 256 with D % 8 == 0, Hkv dividing H with H / Hkv <= 64, window >= 1,
+ *   sinks >= 0, scale > 0 and finite, T*H < 2^31. B, T or H may be 0 (nothing is launched).
+ * ------------------------------------------------------------------------------------------- */
+typedef struct rsm_window_args {
+  int B, T, H, Hkv, D;
+  int window, sinks;
+  rsm_dtype dtype;
+  float scale;
+  const void* q;
+  const void* k;
+  const void* v;
+  void* o;
+  float* lse;
+  int flags; /* RSM_FLAG_* */
+} rsm_window_args;
+
+RSM_API rsm_status rsm_window_forward(const rsm_window_args* args, void* stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * rsm_window_backward -- gradients of rsm_window_forward. With delta_i = dO_i.o_i,
+ * p_ij = e^{s_ij - lse_i} and ds_ij = p_ij (dO_i.v_j - delta_i):
+ *   dq_i = scale sum_j ds_ij k_j;  dk_j = scale sum_i ds_ij q_i;  dv_j = sum_i p_ij dO_i
+ * the sums of dk and dv running over the query heads that share the key/value head, too.
+ *   q, k, v, o, lse: the forward's inputs and outputs;  dO [B,T,H,D] in dtype
+ *   dq [B,T,H,D], dk, dv [B,T,Hkv,D] in dtype (each may be NULL to skip it)
+ *   workspace: at least rsm_window_backward_workspace_size(args) bytes (256-byte aligned); its
+ *     contents are not preserved.
+ *   The gradients are the same, bit for bit, from call to call: no sum is left to the order in
+ *   which blocks finish. Sizes as rsm_window_forward.
+ * ------------------------------------------------------------------------------------------- */
+typedef struct rsm_window_backward_args {
+  int B, T, H, Hkv, D;
+  int window, sinks;
+  rsm_dtype dtype;
+  float scale;
+  const void* q;
+  const void* k;
+  const void* v;
+  const void* o;
+  const float* lse;
+  const void* dO;
+  void* dq;
+  void* dk;
+  void* dv;
+  void* workspace;
+  size_t workspace_bytes;
+  int flags; /* RSM_FLAG_* */
+} rsm_window_backward_args;
+
+/* Bytes of workspace rsm_window_backward needs, or (size_t)-1 for arguments it rejects. Host-only. */
+RSM_API size_t rsm_window_backward_workspace_size(const rsm_window_backward_args* args);
+RSM_API rsm_status rsm_window_backward(const rsm_window_backward_args* args, void* stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * The paged cache. Keys and values of place p of sequence b stand in page
+ * page_table[b][p / page_size], row p % page_size. Sequence b brings n_b = cu_q[b+1] - cu_q[b] new
+ * tokens, which are rows cu_q[b] .. cu_q[b+1]-1 of q, k and v and stand at places
+ * kv_len[b] - n_b .. kv_len[b] - 1: kv_len counts the new tokens. n_b may be 0.
+ *   k_cache, v_cache  [num_pages, page_size, Hkv, D] in dtype
+ *   page_table        [B, table_width] int32
+ *   cu_q              [B + 1] int32, starting at 0 and not falling;  kv_len [B] int32
+ * These three are read on the device and never trusted with an address: an offset outside [0, N] is
+ * clamped; a page outside the cache and places past the table's end are left out (not written, not
+ * seen) and reported as RSM_ERR_BAD_PAGE by rsm_get_device_status. Places below zero are not
+ * written, and a new token at one sees nothing. Rows of o (and lse) behind cu_q[B] keep their bits.
+ *
+ * rsm_paged_append -- writes the new tokens' k and v [N,Hkv,D] to their places. Two tokens must
+ * not share a place (a page in two sequences' tables is fine while neither writes to it).
+ * ------------------------------------------------------------------------------------------- */
+typedef struct rsm_paged_append_args {
+  int B, N, Hkv, D;
+  int num_pages, page_size, table_width;
+  rsm_dtype dtype;
+  const void* k;
+  const void* v;
+  void* k_cache;
+  void* v_cache;
+  const int32_t* page_table;
+  const int32_t* cu_q;
+  const int32_t* kv_len;
+  int flags; /* RSM_FLAG_* (none applies) */
+} rsm_paged_append_args;
+
+RSM_API rsm_status rsm_paged_append(const rsm_paged_append_args* args, void* stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * rsm_paged_forward -- attention of the new tokens over the cache, which already holds their own
+ * keys and values (rsm_paged_append on the same stream). The token at place p sees places j <= p,
+ * and with window > 0 of those only p - j < window or j < sinks (window = 0: no limit, sinks unused).
+ *   q    [N,H,D] in dtype;  o [N,H,D] in dtype;  lse [N,H] fp32 or NULL
+ *   max_q  no sequence has more new tokens than this (tokens past it are not computed: their rows
+ *          keep their bits). With max_q = 1 this is the single-token generation step.
+ *   A row that sees nothing gets o = 0 and lse = -infinity. What the cache holds behind kv_len[b]
+ *   does not matter (it may be NaN); what it holds in front of it must be finite.
+ *   workspace: at least rsm_paged_workspace_size(args) bytes (256-byte aligned; may be NULL when
+ *     that is 0): partial results of long caches that several blocks share.
+ *   Sizes as rsm_window_forward; page_size >= 1, N*H < 2^31, table_width*page_size < 2^31.
+ * ------------------------------------------------------------------------------------------- */
+typedef struct rsm_paged_args {
+  int B, N, max_q, H, Hkv, D;
+  int num_pages, page_size, table_width;
+  int window, sinks;
+  rsm_dtype dtype;
+  float scale;
+  const void* q;
+  const void* k_cache;
+  const void* v_cache;
+  const int32_t* page_table;
+  const int32_t* cu_q;
+  const int32_t* kv_len;
+  void* o;
+  float* lse;
+  void* workspace;
+  size_t workspace_bytes;
+  int flags; /* RSM_FLAG_VALIDATE checks q */
+} rsm_paged_args;
+
+/* Bytes of workspace rsm_paged_forward needs (0 when none), or (size_t)-1 for arguments it rejects.
+ * Host-only. */
+RSM_API size_t rsm_paged_workspace_size(const rsm_paged_args* args);
+RSM_API rsm_status rsm_paged_forward(const rsm_paged_args* args, void* stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * rsm_block_norm_forward -- the norms around a block, with its output gate and residual scale:
+ *   n = y rsqrt(mean(y^2) + eps) w_post         norm of the block's output y
+ *   h = residual + scale n act(gate)            gated, scaled and added to the residual stream
+ *   x = h rsqrt(mean(h^2) + eps) w_pre          norm before the next block (of h before rounding)
+ *   act(g) = g sigmoid(g) (SILU) or sigmoid(g).
+ *   y        [rows,d] in y_dtype (fp32, such as the mixer's o, or dtype)
+ *   gate     [rows,d] in dtype, or NULL for no gate (act is then ignored)
+ *   residual [rows,d] in dtype;  w_post, w_pre [d] fp32 (w_pre NULL: x is not computed)
+ *   h, x     [rows,d] in dtype (x NULL exactly when w_pre is). h may alias residual or, with
+ *            y_dtype = dtype, y.
+ *   Supported: d % 4 == 0, 4 <= d <= 8192, y_dtype = dtype or fp32. rows may be 0.
+ * ------------------------------------------------------------------------------------------- */
+typedef enum rsm_act { RSM_ACT_SILU = 0, RSM_ACT_SIGMOID = 1 } rsm_act;
+
+typedef struct rsm_block_norm_args {
+  int64_t rows;
+  int d;
+  rsm_dtype y_dtype, dtype;
+  rsm_act act;
+  float scale, eps;
+  const void* y;
+  const void* gate;
+  const void* residual;
+  const float* w_post;
+  const float* w_pre;
+  void* h;
+  void* x;
+  int flags; /* RSM_FLAG_* (none applies) */
+} rsm_block_norm_args;
+
+RSM_API rsm_status rsm_block_norm_forward(const rsm_block_norm_args* args, void* stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * rsm_block_norm_backward -- gradients of rsm_block_norm_forward.
+ *   y, gate, residual, w_post, w_pre: the forward's inputs (everything else is recomputed)
+ *   dh, dx   [rows,d] in dtype: gradients of h and x (dh NULL = zero; dx NULL = zero, and needs w_pre
+ *            otherwise)
+ *   dy [rows,d] in y_dtype; dgate (NULL without a gate), dresidual [rows,d] in dtype;
+ *   dw_post, dw_pre [d] fp32 (each output may be NULL to skip it). Outputs must not alias inputs.
+ *   workspace: at least rsm_block_norm_backward_workspace_size(args) bytes (256-byte aligned): the
+ *     blocks' partial sums of dw_post and dw_pre, added up in a fixed order.
+ * ------------------------------------------------------------------------------------------- */
+typedef struct rsm_block_norm_backward_args {
+  int64_t rows;
+  int d;
+  rsm_dtype y_dtype, dtype;
+  rsm_act act;
+  float scale, eps;
+  const void* y;
+  const void* gate;
+  const void* residual;
+  const float* w_post;
+  const float* w_pre;
+  const void* dh;
+  const void* dx;
+  void* dy;
+  void* dgate;
+  void* dresidual;
+  float* dw_post;
+  float* dw_pre;
+  void* workspace;
+  size_t workspace_bytes;
+  int flags; /* RSM_FLAG_* (none applies) */
+} rsm_block_norm_backward_args;
+
+/* Bytes of workspace rsm_block_norm_backward needs, or (size_t)-1 for arguments it rejects. Host-only. */
+RSM_API size_t rsm_block_norm_backward_workspace_size(const rsm_block_norm_backward_args* args);
+RSM_API rsm_status rsm_block_norm_backward(const rsm_block_norm_backward_args* args, void* stream);
+
 /* Human-readable name of a status code (static storage). */
 RSM_API const char* rsm_status_string(rsm_status status);
 
@@ -280,8 +492,8 @@ RSM_API const char* rsm_status_string(rsm_status status);
 RSM_API const char* rsm_last_error(void);
 
 /* Synchronizes `stream`, then reads and clears the library's device status word for the current
- * device: RSM_OK, RSM_ERR_NONFINITE (validation found bad inputs) or RSM_ERR_TIMEOUT (a bounded
- * device wait expired). Errors of the synchronization itself return RSM_ERR_CUDA. */
+ * device: RSM_OK, RSM_ERR_NONFINITE (validation found bad inputs), RSM_ERR_BAD_PAGE (a paged call met a
+ * page or a length outside the cache) or RSM_ERR_TIMEOUT (a bounded device wait expired). Errors of the synchronization itself return RSM_ERR_CUDA. */
 RSM_API rsm_status rsm_get_device_status(void* stream);
 
 /* Library version as major*10000 + minor*100 + patch. */

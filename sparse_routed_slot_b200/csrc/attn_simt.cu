@@ -1,0 +1,544 @@
+// attn_simt.cu -- window and paged attention on CUDA cores, in fp32 (any head dimension, page size
+// and dtype), with its gradients; and the small kernels every attention path shares (delta, the
+// join of split rows, the cache write, the input check).
+//
+// Forward, one block per 64 packed query rows (token, head of the group): the keys pass by in tiles
+// of BB; a running maximum m and sum l per row keep the softmax in one pass,
+//   m' = max(m, max_j s_j),  l' = l e^{m-m'} + sum_j e^{s_j-m'},  acc' = acc e^{m-m'} + sum_j e^{s_j-m'} v_j
+// Backward without atomics, so that its sums have one order: one kernel owns 64 keys and walks the
+// query rows that see them (dk, dv), another owns 64 query rows and walks their keys (dq); both form
+// p = e^{s - lse} and ds = p (dO.v - delta) again, 7 tile products against the 5 of a shared walk.
+//
+// All products have the same two shapes, 64 stationary rows (16 x 16 threads, 4 rows each) against
+// BB streamed ones: W = A B^T over the head dimension and acc += W B. Both read 16-byte pieces of
+// shared memory, the rows padded by 16 bytes so that 8 neighbouring rows use different banks; 8 FMAs
+// per load instruction keep the FMA pipe, not shared memory, the bound.
+#include <algorithm>
+
+#include "attention.cuh"
+
+namespace rsm {
+
+namespace {
+
+using namespace attn;
+
+constexpr int kBA = 64;        // stationary rows
+constexpr int kThreads = 256;  // 16 x 16
+
+template <int DP> struct Tile {
+  // streamed rows per step: 64 where two blocks per SM still fit their tiles, 32 otherwise
+  static constexpr int kBB = DP <= 64 ? 64 : 32;
+};
+
+template <typename T> struct Out;
+template <> struct Out<float> {
+  static RSM_DEV void st4(float* p, float a, float b, float c, float d) {
+    *reinterpret_cast<float4*>(p) = make_float4(a, b, c, d);
+  }
+};
+template <> struct Out<__nv_bfloat16> {
+  static RSM_DEV void st4(__nv_bfloat16* p, float a, float b, float c, float d) {
+    __nv_bfloat162 lo = __floats2bfloat162_rn(a, b), hi = __floats2bfloat162_rn(c, d);
+    *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<uint32_t*>(&lo), *reinterpret_cast<uint32_t*>(&hi));
+  }
+};
+
+// Row r of a tile of n rows comes from base + offset(r) (fp32 in shared memory), or is zero where
+// offset(r) < 0. Columns past D are left alone: no product reads them into a column that is stored.
+template <typename T, int DP, class Off>
+RSM_DEV void load_rows(float* dst, const void* base, int n, int D, Off offset) {
+  const int per = D >> 2;
+  for (int e = threadIdx.x; e < n * per; e += kThreads) {
+    const int r = e / per, c = (e - r * per) << 2;
+    const int64_t off = offset(r);
+    float x[4] = {0.f, 0.f, 0.f, 0.f};
+    if (off >= 0) In<T>::ld4(static_cast<const T*>(base) + off + c, x);
+    *reinterpret_cast<float4*>(dst + r * (DP + 4) + c) = make_float4(x[0], x[1], x[2], x[3]);
+  }
+}
+
+// c[i][j] = sum_d A[ty + 16 i][d] B[tx + 16 j][d]
+template <int DP, int BB>
+RSM_DEV void product_nt(const float* A, const float* B, int D, int tx, int ty, float (&c)[4][BB / 16]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < BB / 16; ++j) c[i][j] = 0.f;
+#pragma unroll 4
+  for (int d = 0; d < D; d += 4) {
+    float4 a[4], b[BB / 16];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4*>(A + (ty + 16 * i) * (DP + 4) + d);
+#pragma unroll
+    for (int j = 0; j < BB / 16; ++j) b[j] = *reinterpret_cast<const float4*>(B + (tx + 16 * j) * (DP + 4) + d);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < BB / 16; ++j) {
+        c[i][j] = fmaf(a[i].x, b[j].x, c[i][j]);
+        c[i][j] = fmaf(a[i].y, b[j].y, c[i][j]);
+        c[i][j] = fmaf(a[i].z, b[j].z, c[i][j]);
+        c[i][j] = fmaf(a[i].w, b[j].w, c[i][j]);
+      }
+  }
+}
+
+// acc[i][jj] += sum_k W[ty + 16 i][k] B[k][4 tx + 64 jj ..]
+template <int DP, int BB>
+RSM_DEV void product_nn(const float* W, const float* B, int tx, int ty, float4 (&acc)[4][DP / 64]) {
+#pragma unroll 2
+  for (int k = 0; k < BB; k += 4) {
+    float4 w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const float4*>(W + (ty + 16 * i) * (BB + 4) + k);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+#pragma unroll
+      for (int jj = 0; jj < DP / 64; ++jj) {
+        const float4 b = *reinterpret_cast<const float4*>(B + (k + u) * (DP + 4) + 4 * tx + 64 * jj);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float x = u == 0 ? w[i].x : u == 1 ? w[i].y : u == 2 ? w[i].z : w[i].w;
+          acc[i][jj].x = fmaf(x, b.x, acc[i][jj].x);
+          acc[i][jj].y = fmaf(x, b.y, acc[i][jj].y);
+          acc[i][jj].z = fmaf(x, b.z, acc[i][jj].z);
+          acc[i][jj].w = fmaf(x, b.w, acc[i][jj].w);
+        }
+      }
+    }
+  }
+}
+
+RSM_DEV float half_warp_max(float v) {
+#pragma unroll
+  for (int d = 8; d >= 1; d >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, d));
+  return v;
+}
+RSM_DEV float half_warp_sum(float v) {
+#pragma unroll
+  for (int d = 8; d >= 1; d >>= 1) v += __shfl_xor_sync(kFull, v, d);
+  return v;
+}
+
+constexpr float kNegInf = -__builtin_inff();
+
+template <typename T, int DP>
+__global__ void __launch_bounds__(kThreads) attn_simt_kernel(const AttnParams p, int ntiles) {
+  constexpr int BB = Tile<DP>::kBB;
+  extern __shared__ float sm[];
+  float* sQ = sm;
+  float* sK = sQ + kBA * (DP + 4);
+  float* sV = sK + BB * (DP + 4);
+  float* sP = sV + BB * (DP + 4);
+  const int split = blockIdx.x % p.splits;
+  const int item = blockIdx.x / p.splits;
+  const int tile = item % ntiles, pair = item / ntiles;
+  const int hk = pair % p.Hkv, b = pair / p.Hkv;
+  const Seq s = sequence(p, b);
+  if (s.kv != s.pos0 + s.nq && threadIdx.x == 0 && p.table) raise_status(RSM_ERR_BAD_PAGE);
+  const int nq = p.table ? min(s.nq, p.max_q) : s.nq;
+  const int r0 = tile * kBA;
+  const int rows = (int)min((int64_t)nq * p.G - r0, (int64_t)kBA);
+  if (rows <= 0) return;
+  const int G = p.G, D = p.D;
+  auto q_index = [&](int r) { return (s.row0 + (r0 + r) / G) * p.H + hk * G + (r0 + r) % G; };
+  load_rows<T, DP>(sQ, p.q, kBA, D, [&](int r) { return r < rows ? q_index(r) * D : (int64_t)-1; });
+
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  int pos[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) pos[i] = s.pos0 + (r0 + ty + 16 * i) / G;
+  const Walk walk = key_walk(s.pos0 + r0 / G, s.pos0 + (r0 + rows - 1) / G, s.kv, p.window, p.sinks, BB);
+  const int w0 = (int)((int64_t)walk.n * split / p.splits), w1 = (int)((int64_t)walk.n * (split + 1) / p.splits);
+
+  const float scale2 = p.scale * kLog2e;
+  float m[4], l[4];
+  float4 acc[4][DP / 64];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    m[i] = kNegInf;
+    l[i] = 0.f;
+#pragma unroll
+    for (int jj = 0; jj < DP / 64; ++jj) acc[i][jj] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  for (int w = w0; w < w1; ++w) {
+    const int k0 = walk.tile(w) * BB;
+    __syncthreads();
+    // rows behind the last key are zero, so that a weight of zero meets no stale NaN
+    auto off = [&](int r) { return k0 + r < s.kv ? kv_offset(p, b, hk, k0 + r) : (int64_t)-1; };
+    load_rows<T, DP>(sK, p.k, BB, D, off);
+    load_rows<T, DP>(sV, p.v, BB, D, off);
+    __syncthreads();
+    float c[4][BB / 16];
+    product_nt<DP, BB>(sQ, sK, D, tx, ty, c);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float top = kNegInf;
+#pragma unroll
+      for (int j = 0; j < BB / 16; ++j) {
+        const int key = k0 + tx + 16 * j;
+        bool seen = key < s.kv && sees(pos[i], key, p.window, p.sinks);
+        if (seen && p.table) seen = kv_offset(p, b, hk, key) >= 0;
+        c[i][j] = seen ? c[i][j] * scale2 : kNegInf;
+        top = fmaxf(top, c[i][j]);
+      }
+      const float mn = fmaxf(m[i], half_warp_max(top));
+      const float ref = mn == kNegInf ? 0.f : mn;  // nothing seen yet: every weight below is e^-inf = 0
+      const float corr = exp2f(m[i] - ref);
+      m[i] = mn;
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < BB / 16; ++j) {
+        const float x = exp2f(c[i][j] - ref);
+        sum += x;
+        sP[(ty + 16 * i) * (BB + 4) + tx + 16 * j] = x;
+      }
+      l[i] = l[i] * corr + half_warp_sum(sum);
+#pragma unroll
+      for (int jj = 0; jj < DP / 64; ++jj) {
+        acc[i][jj].x *= corr; acc[i][jj].y *= corr; acc[i][jj].z *= corr; acc[i][jj].w *= corr;
+      }
+    }
+    __syncwarp();  // a row of P is written and read by the same half warp
+    product_nn<DP, BB>(sP, sV, tx, ty, acc);
+  }
+  const int64_t total = (int64_t)p.T * (p.table ? 1 : p.B) * p.H;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = ty + 16 * i;
+    if (r >= rows) continue;
+    const int64_t at = q_index(r);
+    const float inv = l[i] > 0.f ? 1.f / l[i] : l[i] == 0.f ? 0.f : l[i];  // (a NaN stays one)
+    const float lse = l[i] == 0.f ? kNegInf : (m[i] + log2f(l[i])) * kLn2;
+#pragma unroll
+    for (int jj = 0; jj < DP / 64; ++jj) {
+      const int d = 4 * tx + 64 * jj;
+      if (d >= D) continue;
+      const float4 a = acc[i][jj];
+      if (p.splits > 1)
+        Out<float>::st4(p.part_o + (split * total + at) * D + d, a.x * inv, a.y * inv, a.z * inv, a.w * inv);
+      else
+        Out<T>::st4(static_cast<T*>(p.o) + at * D + d, a.x * inv, a.y * inv, a.z * inv, a.w * inv);
+    }
+    if (tx == 0) {
+      if (p.splits > 1) p.part_lse[split * total + at] = lse;
+      else if (p.lse) p.lse[at] = lse;
+    }
+  }
+}
+
+// Gradients. DQ: the stationary rows are query rows (A1 = q, A2 = dO), the streamed ones keys
+// (B1 = k, B2 = v) and acc2 = dq. Otherwise the stationary rows are keys (k, v), the streamed ones
+// query rows (q, dO), acc1 = dv and acc2 = dk.
+template <typename T, int DP, bool DQ>
+__global__ void __launch_bounds__(kThreads) attn_simt_backward_kernel(const AttnParams p, int ntiles) {
+  constexpr int BB = 32;
+  extern __shared__ float sm[];
+  float* sA1 = sm;
+  float* sA2 = sA1 + kBA * (DP + 4);
+  float* sB1 = sA2 + kBA * (DP + 4);
+  float* sB2 = sB1 + BB * (DP + 4);
+  float* sW2 = sB2 + BB * (DP + 4);
+  float* sW1 = sW2 + kBA * (BB + 4);              // DQ: not used
+  float* sStat = DQ ? sW1 : sW1 + kBA * (BB + 4);  // lse (base 2) and delta of the query rows
+  const int tile = blockIdx.x % ntiles, pair = blockIdx.x / ntiles;
+  const int hk = pair % p.Hkv, b = pair / p.Hkv;
+  const int G = p.G, D = p.D, T_ = p.T;
+  const int64_t nrows = (int64_t)T_ * G;  // packed query rows of this pair (< 2^31)
+  const int a0 = tile * kBA;
+  auto q_index = [&](int64_t r) { return ((int64_t)b * T_ + r / G) * p.H + hk * G + r % G; };
+  auto q_off = [&](int64_t r) { return r < nrows ? q_index(r) * D : (int64_t)-1; };
+  auto k_off = [&](int key) { return key < T_ ? kv_offset(p, b, hk, key) : (int64_t)-1; };
+  auto load_stats = [&](int64_t r0, int n) {
+    for (int r = threadIdx.x; r < n; r += kThreads) {
+      const bool in = r0 + r < nrows;
+      sStat[2 * r] = in ? p.lse[q_index(r0 + r)] * kLog2e : 0.f;
+      sStat[2 * r + 1] = in ? p.delta[q_index(r0 + r)] : 0.f;
+    }
+  };
+  Walk walk{0, 0, 0};
+  if (DQ) {
+    load_rows<T, DP>(sA1, p.q, kBA, D, [&](int r) { return q_off(a0 + r); });
+    load_rows<T, DP>(sA2, p.dO, kBA, D, [&](int r) { return q_off(a0 + r); });
+    load_stats(a0, kBA);
+    walk = key_walk(a0 / G, (int)(min(nrows, (int64_t)a0 + kBA) - 1) / G, T_, p.window, p.sinks, BB);
+  } else {
+    load_rows<T, DP>(sA1, p.k, kBA, D, [&](int r) { return k_off(a0 + r); });
+    load_rows<T, DP>(sA2, p.v, kBA, D, [&](int r) { return k_off(a0 + r); });
+    int t0, t1;
+    query_range(a0, min(a0 + kBA, T_) - 1, T_, p.window, p.sinks, t0, t1);
+    walk.first = t0 * G / BB;
+    walk.n = (int)(((int64_t)t1 * G - 1) / BB) + 1 - walk.first;
+  }
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const float scale2 = p.scale * kLog2e;
+  float4 acc1[DQ ? 1 : 4][DP / 64], acc2[4][DP / 64];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int jj = 0; jj < DP / 64; ++jj) {
+      if (!DQ) acc1[DQ ? 0 : i][jj] = make_float4(0.f, 0.f, 0.f, 0.f);
+      acc2[i][jj] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+  for (int w = 0; w < walk.n; ++w) {
+    const int b0 = walk.tile(w) * BB;
+    __syncthreads();
+    if (DQ) {
+      load_rows<T, DP>(sB1, p.k, BB, D, [&](int r) { return k_off(b0 + r); });
+      load_rows<T, DP>(sB2, p.v, BB, D, [&](int r) { return k_off(b0 + r); });
+    } else {
+      load_rows<T, DP>(sB1, p.q, BB, D, [&](int r) { return q_off(b0 + r); });
+      load_rows<T, DP>(sB2, p.dO, BB, D, [&](int r) { return q_off(b0 + r); });
+      load_stats(b0, BB);
+    }
+    __syncthreads();
+    float c1[4][BB / 16], c2[4][BB / 16];
+    product_nt<DP, BB>(sA1, sB1, D, tx, ty, c1);
+    product_nt<DP, BB>(sA2, sB2, D, tx, ty, c2);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+      for (int j = 0; j < BB / 16; ++j) {
+        const int ra = ty + 16 * i, rb = tx + 16 * j;
+        const int key = DQ ? b0 + rb : a0 + ra;
+        const int row = DQ ? a0 + ra : b0 + rb;
+        const float* st = sStat + 2 * (DQ ? ra : rb);
+        const bool seen = row < nrows && key < T_ && sees(row / G, key, p.window, p.sinks);
+        const float pr = seen ? exp2f(c1[i][j] * scale2 - st[0]) : 0.f;
+        const float ds = seen ? pr * (c2[i][j] - st[1]) : 0.f;
+        sW2[ra * (BB + 4) + rb] = ds;
+        if (!DQ) sW1[ra * (BB + 4) + rb] = pr;
+      }
+    }
+    __syncwarp();  // a row of the weights is written and read by the same half warp
+    product_nn<DP, BB>(sW2, sB1, tx, ty, acc2);
+    if constexpr (!DQ) product_nn<DP, BB>(sW1, sB2, tx, ty, acc1);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t r = a0 + ty + 16 * i;
+    const int64_t off = DQ ? q_off(r) : k_off((int)r);
+    if (off < 0) continue;
+#pragma unroll
+    for (int jj = 0; jj < DP / 64; ++jj) {
+      const int d = 4 * tx + 64 * jj;
+      if (d >= D) continue;
+      const float4 a = acc2[i][jj];
+      T* g = static_cast<T*>(DQ ? p.dq : p.dk);
+      if (g) Out<T>::st4(g + off + d, a.x * p.scale, a.y * p.scale, a.z * p.scale, a.w * p.scale);
+      if (!DQ && p.dv) {
+        const float4 v = acc1[DQ ? 0 : i][jj];
+        Out<T>::st4(static_cast<T*>(p.dv) + off + d, v.x, v.y, v.z, v.w);
+      }
+    }
+  }
+}
+
+// delta = dO . o, a warp per row.
+template <typename T>
+__global__ void __launch_bounds__(256) delta_kernel(const T* dO, const T* o, float* delta, int64_t rows, int D) {
+  const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (row >= rows) return;
+  const int lane = threadIdx.x & 31;
+  float sum = 0.f;
+  for (int d = lane * 4; d < D; d += 128) {
+    float a[4], x[4];
+    In<T>::ld4(dO + row * D + d, a);
+    In<T>::ld4(o + row * D + d, x);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sum = fmaf(a[i], x[i], sum);
+  }
+  sum = warp_sum_f(sum);
+  if (lane == 0) delta[row] = sum;
+}
+
+// o = sum_s e^{lse_s - lse} o_s over the splits, a warp per row. Rows that no block computed (behind
+// the last sequence, or past max_q) are left alone.
+template <typename T>
+__global__ void __launch_bounds__(256) combine_kernel(const AttnParams p) {
+  const int64_t total = (int64_t)p.T * p.H;
+  const int64_t at = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (at >= total) return;
+  const int lane = threadIdx.x & 31;
+  const int tok = (int)(at / p.H);
+  // the token's sequence: the last b with cu_q[b] <= tok
+  int lo = 0, hi = p.B;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (p.cu_q[mid] <= tok) lo = mid; else hi = mid;
+  }
+  const Seq s = sequence(p, lo);
+  if (tok < s.row0 || tok >= s.row0 + min(s.nq, p.max_q)) return;
+  float top = kNegInf;
+  for (int i = lane; i < p.splits; i += 32) top = fmaxf(top, p.part_lse[i * total + at]);
+  top = warp_max_f(top);
+  const float ref = top == kNegInf ? 0.f : top;
+  float sum = 0.f;
+  for (int i = lane; i < p.splits; i += 32) sum += expf(p.part_lse[i * total + at] - ref);
+  sum = warp_sum_f(sum);
+  const float inv = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;
+  for (int d = lane * 4; d < p.D; d += 128) {
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < p.splits; ++i) {
+      const float w = expf(p.part_lse[i * total + at] - ref) * inv;
+      if (w == 0.f) continue;
+      const float4 x = *reinterpret_cast<const float4*>(p.part_o + (i * total + at) * p.D + d);
+      a.x = fmaf(w, x.x, a.x); a.y = fmaf(w, x.y, a.y); a.z = fmaf(w, x.z, a.z); a.w = fmaf(w, x.w, a.w);
+    }
+    Out<T>::st4(static_cast<T*>(p.o) + at * p.D + d, a.x, a.y, a.z, a.w);
+  }
+  if (lane == 0 && p.lse) p.lse[at] = sum == 0.f ? kNegInf : ref + logf(sum);
+}
+
+// Writes the new tokens' rows of Hkv*D elements to their places, 16 bytes per thread and step; a row
+// is contiguous on both sides. Bound by the copy itself (2 reads and 2 writes of the rows).
+__global__ void __launch_bounds__(256) append_kernel(const rsm_paged_append_args a, int chunks) {
+  const int64_t n = (int64_t)a.N * chunks;
+  for (int64_t e = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; e < n; e += (int64_t)gridDim.x * blockDim.x) {
+    const int tok = (int)(e / chunks);
+    const int c = (int)(e - (int64_t)tok * chunks);
+    int lo = 0, hi = a.B;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (a.cu_q[mid] <= tok) lo = mid; else hi = mid;
+    }
+    const int c0 = max(a.cu_q[lo], 0), c1 = min(a.cu_q[lo + 1], a.N);
+    if (tok < c0 || tok >= c1) continue;
+    const int64_t pos = (int64_t)max(a.kv_len[lo], 0) - (c1 - tok);
+    if (pos < 0) continue;
+    const int64_t slot = pos / a.page_size;
+    const int pg = slot < a.table_width ? a.page_table[(int64_t)lo * a.table_width + slot] : -1;
+    if ((unsigned)pg >= (unsigned)a.num_pages) {
+      raise_status(RSM_ERR_BAD_PAGE);
+      continue;
+    }
+    const int64_t to = ((int64_t)pg * a.page_size + pos % a.page_size) * chunks + c;
+    static_cast<uint4*>(a.k_cache)[to] = static_cast<const uint4*>(a.k)[e];
+    static_cast<uint4*>(a.v_cache)[to] = static_cast<const uint4*>(a.v)[e];
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256) check_finite_kernel(const T* x, int64_t n) {
+  bool bad = false;
+  for (int64_t e = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; e < n; e += (int64_t)gridDim.x * blockDim.x)
+    bad |= !finite_f32(In<T>::ld(x + e));
+  if (bad) raise_status(RSM_ERR_NONFINITE);
+}
+
+int64_t all_rows(const AttnParams& p) { return (int64_t)p.T * (p.table ? 1 : p.B) * p.H; }
+
+int64_t row_tiles(const AttnParams& p) {
+  const int64_t nq = p.table ? p.max_q : p.T;
+  return (nq * p.G + kBA - 1) / kBA;
+}
+
+template <typename T, int DP>
+cudaError_t forward_dp(const AttnParams& p, cudaStream_t stream) {
+  constexpr int BB = Tile<DP>::kBB;
+  constexpr int bytes = ((kBA + 2 * BB) * (DP + 4) + kBA * (BB + 4)) * 4;
+  cudaError_t e = set_smem_limit<attn_simt_kernel<T, DP>>(bytes);
+  if (e != cudaSuccess) return e;
+  const int64_t nt = row_tiles(p);
+  const int64_t grid = nt * p.Hkv * p.B * p.splits;
+  if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  attn_simt_kernel<T, DP><<<(unsigned)grid, kThreads, bytes, stream>>>(p, (int)nt);
+  return cudaGetLastError();
+}
+
+template <typename T, int DP>
+cudaError_t backward_dp(const AttnParams& p, cudaStream_t stream) {
+  constexpr int BB = 32;
+  constexpr int bytes = ((2 * kBA + 2 * BB) * (DP + 4) + 2 * kBA * (BB + 4) + 2 * kBA) * 4;
+  static_assert(bytes <= 232448, "shared memory budget");
+  if (p.dk || p.dv) {
+    cudaError_t e = set_smem_limit<attn_simt_backward_kernel<T, DP, false>>(bytes);
+    if (e != cudaSuccess) return e;
+    const int nt = (p.T + kBA - 1) / kBA;
+    const int64_t grid = (int64_t)nt * p.Hkv * p.B;
+    if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    attn_simt_backward_kernel<T, DP, false><<<(unsigned)grid, kThreads, bytes, stream>>>(p, nt);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  if (p.dq) {
+    cudaError_t e = set_smem_limit<attn_simt_backward_kernel<T, DP, true>>(bytes);
+    if (e != cudaSuccess) return e;
+    const int64_t nt = row_tiles(p);
+    const int64_t grid = nt * p.Hkv * p.B;
+    if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    attn_simt_backward_kernel<T, DP, true><<<(unsigned)grid, kThreads, bytes, stream>>>(p, (int)nt);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace
+
+cudaError_t launch_attn_simt(const AttnParams& p, rsm_dtype dtype, cudaStream_t stream) {
+  if (dtype == RSM_F32)
+    return p.D <= 64 ? forward_dp<float, 64>(p, stream)
+                     : p.D <= 128 ? forward_dp<float, 128>(p, stream) : forward_dp<float, 256>(p, stream);
+  return p.D <= 64 ? forward_dp<__nv_bfloat16, 64>(p, stream)
+                   : p.D <= 128 ? forward_dp<__nv_bfloat16, 128>(p, stream) : forward_dp<__nv_bfloat16, 256>(p, stream);
+}
+
+cudaError_t launch_attn_simt_backward(const AttnParams& p, rsm_dtype dtype, cudaStream_t stream) {
+  if (dtype == RSM_F32)
+    return p.D <= 64 ? backward_dp<float, 64>(p, stream)
+                     : p.D <= 128 ? backward_dp<float, 128>(p, stream) : backward_dp<float, 256>(p, stream);
+  return p.D <= 64 ? backward_dp<__nv_bfloat16, 64>(p, stream)
+                   : p.D <= 128 ? backward_dp<__nv_bfloat16, 128>(p, stream)
+                                : backward_dp<__nv_bfloat16, 256>(p, stream);
+}
+
+cudaError_t launch_attn_delta(const AttnParams& p, rsm_dtype dtype, cudaStream_t stream) {
+  const int64_t rows = all_rows(p);
+  const unsigned grid = (unsigned)((rows + 7) / 8);
+  if (dtype == RSM_F32)
+    delta_kernel<float><<<grid, 256, 0, stream>>>(static_cast<const float*>(p.dO), static_cast<const float*>(p.o),
+                                                  p.delta, rows, p.D);
+  else
+    delta_kernel<__nv_bfloat16><<<grid, 256, 0, stream>>>(static_cast<const __nv_bfloat16*>(p.dO),
+                                                          static_cast<const __nv_bfloat16*>(p.o), p.delta, rows, p.D);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_attn_combine(const AttnParams& p, rsm_dtype dtype, cudaStream_t stream) {
+  const unsigned grid = (unsigned)((all_rows(p) + 7) / 8);
+  if (dtype == RSM_F32) combine_kernel<float><<<grid, 256, 0, stream>>>(p);
+  else combine_kernel<__nv_bfloat16><<<grid, 256, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+// Blocks that share the keys of a row: enough for two blocks per SM where there are few rows, and
+// never under 4 key tiles each. The cache's length is known on the device alone; the table's width
+// bounds it, and each block takes its share of the real length.
+int attn_simt_splits(const AttnParams& p) {
+  if (!p.table) return 1;
+  const int64_t blocks = std::max<int64_t>(1, row_tiles(p) * p.Hkv * p.B);
+  int64_t keys = (int64_t)p.table_width * p.page;
+  if (p.window > 0) keys = std::min<int64_t>(keys, (int64_t)p.window + p.sinks + p.max_q);
+  const int64_t tiles = (keys + 31) / 32;
+  const int64_t want = (2 * device_sm_count() + blocks - 1) / blocks;
+  return (int)std::max<int64_t>(1, std::min<int64_t>({want, tiles / 4, 64}));
+}
+
+cudaError_t launch_paged_append(const rsm_paged_append_args& a, cudaStream_t stream) {
+  const int chunks = (int)((int64_t)a.Hkv * a.D * (a.dtype == RSM_F32 ? 4 : 2) / 16);
+  const int64_t n = (int64_t)a.N * chunks;
+  const int64_t grid = std::min<int64_t>((n + 255) / 256, 8 * (int64_t)device_sm_count());
+  append_kernel<<<(unsigned)grid, 256, 0, stream>>>(a, chunks);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_check_finite(const void* x, int64_t n, rsm_dtype dtype, cudaStream_t stream) {
+  const unsigned grid = (unsigned)std::min<int64_t>((n + 255) / 256, 8 * (int64_t)device_sm_count());
+  if (dtype == RSM_F32) check_finite_kernel<float><<<grid, 256, 0, stream>>>(static_cast<const float*>(x), n);
+  else check_finite_kernel<__nv_bfloat16><<<grid, 256, 0, stream>>>(static_cast<const __nv_bfloat16*>(x), n);
+  return cudaGetLastError();
+}
+
+}  // namespace rsm

@@ -125,6 +125,7 @@ const char* rsm_status_string(rsm_status s) {
     case RSM_ERR_NONFINITE: return "RSM_ERR_NONFINITE";
     case RSM_ERR_WORKSPACE: return "RSM_ERR_WORKSPACE";
     case RSM_ERR_TIMEOUT: return "RSM_ERR_TIMEOUT";
+    case RSM_ERR_BAD_PAGE: return "RSM_ERR_BAD_PAGE";
   }
   return "RSM_ERR_UNKNOWN";
 }
@@ -325,7 +326,8 @@ rsm_status rsm_get_device_status(void* stream) {
   if (e == cudaSuccess) e = cudaStreamSynchronize(st);
   if (e != cudaSuccess) return cuda_fail(e, "rsm_get_device_status copy");
   if (word & (1u << RSM_ERR_TIMEOUT)) return fail(RSM_ERR_TIMEOUT, "a bounded device wait expired");
-  if (word & (1u << RSM_ERR_NONFINITE)) return fail(RSM_ERR_NONFINITE, "validation found a non-finite logit or f, or f > 0");
+  if (word & (1u << RSM_ERR_BAD_PAGE)) return fail(RSM_ERR_BAD_PAGE, "a page table entry or a length points outside the cache");
+  if (word & (1u << RSM_ERR_NONFINITE)) return fail(RSM_ERR_NONFINITE, "validation found a non-finite input, or f > 0");
   return RSM_OK;
 }
 

@@ -42,6 +42,51 @@ size_t prefill_tc_workspace_bytes(const rsm_forward_args& a);
 int prefill_tc_launches(const rsm_forward_args& a);  // kernel launches of one call
 cudaError_t launch_prefill_tc(const rsm_forward_args& a, cudaStream_t stream);
 
+// Attention (window and paged). One parameter block serves every attention kernel: `table` is null
+// for dense [B,T,...] tensors (T = tokens of a sequence) and set for a paged cache (T = N, all new
+// tokens; k and v are the caches).
+struct AttnParams {
+  int B, T, H, Hkv, G, D;
+  int window, sinks;  // window <= 0: no limit
+  float scale;
+  const void* q;
+  const void* k;
+  const void* v;
+  void* o;
+  float* lse;
+  const int32_t* table;
+  const int32_t* cu_q;
+  const int32_t* kv_len;
+  int num_pages, page, table_width;
+  int max_q;
+  int splits;         // blocks that share a row's keys; > 1: partial results below
+  float* part_o;      // [splits][rows][D], normalised
+  float* part_lse;    // [splits][rows]
+  // backward
+  const void* dO;
+  void* dq;
+  void* dk;
+  void* dv;
+  float* delta;       // [rows]: dO . o
+};
+
+// CUDA-core kernels in fp32 (any dtype, head dimension and page size).
+int attn_simt_splits(const AttnParams& p);
+cudaError_t launch_attn_simt(const AttnParams& p, rsm_dtype dtype, cudaStream_t stream);
+cudaError_t launch_attn_simt_backward(const AttnParams& p, rsm_dtype dtype, cudaStream_t stream);
+// delta = dO . o for every row (the first step of every backward).
+cudaError_t launch_attn_delta(const AttnParams& p, rsm_dtype dtype, cudaStream_t stream);
+// Joins the partial results of p.splits blocks into o and lse.
+cudaError_t launch_attn_combine(const AttnParams& p, rsm_dtype dtype, cudaStream_t stream);
+cudaError_t launch_paged_append(const rsm_paged_append_args& a, cudaStream_t stream);
+// Raises RSM_ERR_NONFINITE when one of n values is not finite.
+cudaError_t launch_check_finite(const void* x, int64_t n, rsm_dtype dtype, cudaStream_t stream);
+
+// Norms around a block (block_norm.cu).
+cudaError_t launch_block_norm(const rsm_block_norm_args& a, cudaStream_t stream);
+size_t block_norm_backward_workspace_bytes(const rsm_block_norm_backward_args& a);
+cudaError_t launch_block_norm_backward(const rsm_block_norm_backward_args& a, cudaStream_t stream);
+
 // Profiling events of the calling host thread (rsm_forward_set_profile_events): when set, launch
 // functions record event i after their i-th kernel (event 0 before the first).
 struct ProfileEvents {

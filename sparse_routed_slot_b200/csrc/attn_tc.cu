@@ -1,0 +1,496 @@
+// attn_tc.cu -- window and paged attention of bf16 inputs on the 5th-generation tensor cores.
+//
+// One block owns two tiles of 128 packed query rows (token, head of the group) of one key/value head
+// and walks the keys they see in tiles of 128:
+//   S = Q K^T            tcgen05.mma, both operands from shared memory, fp32 in TMEM
+//   P = 2^(S' - m)       S' = scale log2(e) S; the row's thread reads S from TMEM and writes P back as
+//                        bf16 over the same columns (the softmax weights are rounded here: the second
+//                        product takes bf16, and 2^-9 per weight is below what bf16 outputs keep)
+//   O += P V             P from TMEM, V as the tile TMA wrote it (contracted over its rows), fp32 in TMEM
+// The reference m of a row moves only when the running maximum has passed it by 2^8, so O is rescaled
+// once or twice per row instead of per tile; sums are of the fp32 weights and stay below 128 * 2^8 a tile.
+//
+// Two tiles because they take turns: while one tile's 128 threads do their exponentials, the tensor core
+// multiplies for the other. Per 128 x 128 tile and head dimension 128 the two products take 1024 tensor
+// cycles and the exponentials 1024 of the special function units, so neither leaves room for the other
+// to wait. K and V tiles serve both query tiles.
+//
+// Warps: 0-3 and 4-7 the rows of tiles 0 and 1 (a thread per row), 8 copies (TMA), 9 MMA issuer.
+// TMEM columns: S (and P) of the tiles at 0 and 128, O at 256 and 256 + DP.
+// A paged cache is read page by page (page sizes that divide 128 or are multiples of it, from 8 on): a
+// tile is 128 / page copies. Rows of V behind the last key are cleared before P multiplies them, so what
+// the cache holds there does not matter.
+#include <cuda.h>
+
+#include <algorithm>
+
+#include "attention.cuh"
+#include "tc.cuh"
+#include "tma_map.h"
+
+namespace rsm {
+
+namespace {
+
+using namespace attn;
+
+constexpr int kBM = 128, kBN = 128;
+constexpr int kThreads = 320;
+constexpr int kCopyWarp = 8, kMmaWarp = 9;
+constexpr float kNegInf = -__builtin_inff();
+constexpr float kSlack = 8.f;  // how far (log2) the running maximum may pass the reference
+
+struct Maps {
+  CUtensorMap q, k, v;
+};
+
+template <int DP> struct Layout {
+  static constexpr int kStages = DP == 64 ? 4 : 2;
+  static constexpr int kTile = kBM * DP * 2;  // bytes of one operand tile
+  static constexpr int kOffK = 2 * kTile;
+  static constexpr int kOffV = kOffK + kStages * kTile;
+  static constexpr int kBytes = kOffV + kStages * kTile + 1024;
+  static_assert(kBytes <= 232448 - 1024, "shared memory budget");
+};
+
+RSM_DEV void mbar_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(tc::smem_u32(bar)) : "memory");
+}
+
+// Bounded wait of a whole warp. False: the wait expired here or somewhere else in the block.
+RSM_DEV bool wait_ok(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  if (!tc::mbar_wait(bar, parity)) {
+    *abort_flag = 1;
+    raise_status(RSM_ERR_TIMEOUT);
+  }
+  return !__any_sync(kFull, *abort_flag != 0);
+}
+
+RSM_DEV float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+RSM_DEV uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 t = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&t);
+}
+
+// The key tiles that one query tile of the block sees.
+struct Active {
+  int ns, first, last;
+  RSM_DEV bool operator()(int tile) const { return tile <= last && (tile < ns || tile >= first); }
+};
+
+RSM_DEV Active active_tiles(int p0, int p1, int kv, const AttnParams& p, bool any) {
+  const Walk w = key_walk(p0, p1, kv, p.window, p.sinks, kBN);
+  if (!any || w.n == 0) return {0, 0, -1};
+  return {w.ns, w.first, w.n > w.ns ? w.first + (w.n - w.ns) - 1 : w.ns - 1};
+}
+
+template <int DP, bool PAGED>
+__global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_constant__ Maps maps, const AttnParams p,
+                                                              int tok_tile, int npairs) {
+  using L = Layout<DP>;
+  constexpr int NS = L::kStages;
+  constexpr int kBlocks = DP / 64;  // 64-column blocks of a tile
+  extern __shared__ unsigned char smem_raw[];
+  __shared__ uint64_t q_full[2], k_full[NS], k_empty[NS], v_full[NS], v_empty[NS], s_full[2], p_full[2], fin[2];
+  __shared__ uint32_t bad_pages[NS];
+  __shared__ uint32_t s_tbase;
+  __shared__ int s_abort;
+
+  // the last query tiles see the most keys: they start first
+  const int split = blockIdx.x % p.splits;
+  const int item = blockIdx.x / p.splits;
+  const int pair = npairs - 1 - item % npairs;
+  const int hk = item / npairs % p.Hkv, b = item / npairs / p.Hkv;
+  const Seq s = sequence(p, b);
+  if (PAGED && s.kv != s.pos0 + s.nq && threadIdx.x == 0) raise_status(RSM_ERR_BAD_PAGE);
+  const int nq = PAGED ? min(s.nq, p.max_q) : s.nq;
+  const int tok0 = pair * 2 * tok_tile;
+  if (tok0 >= nq) return;
+  const int G = p.G, D = p.D;
+  const int ntok0 = min(tok_tile, nq - tok0), ntok1 = max(0, min(tok_tile, nq - tok0 - tok_tile));
+  const int pos0 = s.pos0 + tok0;
+  const Walk walk = key_walk(pos0, pos0 + ntok0 + ntok1 - 1, s.kv, p.window, p.sinks, kBN);
+  const int w0 = (int)((int64_t)walk.n * split / p.splits), w1 = (int)((int64_t)walk.n * (split + 1) / p.splits);
+  const int n = w1 - w0;
+  Active act[2] = {active_tiles(pos0, pos0 + ntok0 - 1, s.kv, p, true),
+                   active_tiles(pos0 + tok_tile, pos0 + tok_tile + ntok1 - 1, s.kv, p, ntok1 > 0)};
+
+  unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp == kMmaWarp) tc::tmem_alloc(&s_tbase, 512);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&q_full[i], 1);
+      tc::mbar_init(&s_full[i], 1);
+      tc::mbar_init(&p_full[i], kBM);
+      tc::mbar_init(&fin[i], 1);
+    }
+    for (int i = 0; i < NS; ++i) {
+      tc::mbar_init(&k_full[i], 1);
+      tc::mbar_init(&k_empty[i], 1);
+      tc::mbar_init(&v_full[i], 1);
+      tc::mbar_init(&v_empty[i], 1);
+    }
+    tc::fence_mbar_init();
+    s_abort = 0;
+  }
+  tc::tmem_fence_before();
+  __syncthreads();
+  tc::tmem_fence_after();
+  const uint32_t tb = s_tbase;
+  volatile int* abort_flag = &s_abort;
+
+  if (warp == kCopyWarp) {
+    // =========================================================================== copies
+    if (lane == 0) {
+      tc::tma_prefetch_desc(&maps.q);
+      tc::tma_prefetch_desc(&maps.k);
+      tc::tma_prefetch_desc(&maps.v);
+      const uint32_t qbytes = (uint32_t)(tok_tile * G * 128 * kBlocks);
+      for (int t = 0; t < (ntok1 > 0 ? 2 : 1); ++t) {
+        tc::mbar_arrive_expect_tx(&q_full[t], qbytes);
+        const int64_t tok = (PAGED ? s.row0 : 0) + tok0 + t * tok_tile;
+        for (int c = 0; c < kBlocks; ++c)
+          tc::tma_load_4d(sm + t * L::kTile + c * (kBM * 128), &maps.q, &q_full[t], 64 * c, hk * G, (int)tok,
+                          PAGED ? 0 : b);
+      }
+    }
+    __syncwarp();
+    int issued = 0;  // K tiles whose copies were started (V follows its K)
+    for (int i = 0; i < n; ++i) {
+      const int st = i % NS, round = i / NS;
+      const int k0 = walk.tile(w0 + i) * kBN;
+      int page_id = 0;
+      uint32_t wanted = 1, bad = 0;
+      const int rows = PAGED ? min(p.page, kBN) : kBN;  // rows of one copy
+      if (PAGED) {
+        // lane l fetches page l of the tile
+        const int key = k0 + lane * rows;
+        const bool in = lane * rows < kBN && key < s.kv;
+        if (in) page_id = p.table[(int64_t)b * p.table_width + key / p.page];
+        const bool ok = in && (unsigned)page_id < (unsigned)p.num_pages;
+        wanted = __ballot_sync(kFull, ok);
+        bad = __ballot_sync(kFull, in && !ok);
+        if (bad && lane == 0) raise_status(RSM_ERR_BAD_PAGE);
+      }
+      auto copy = [&](uint64_t* full, const CUtensorMap* map, unsigned char* dst) {
+        if (lane == 0) tc::mbar_arrive_expect_tx(full, (uint32_t)__popc(wanted) * rows * 128 * kBlocks);
+        __syncwarp();
+        if ((wanted >> lane) & 1) {
+          for (int c = 0; c < kBlocks; ++c) {
+            if (PAGED)
+              tc::tma_load_4d(dst + c * (kBN * 128) + lane * rows * 128, map, full, 64 * c, hk,
+                              p.page > kBN ? k0 % p.page : 0, page_id);
+            else
+              tc::tma_load_4d(dst + c * (kBN * 128), map, full, 64 * c, hk, k0, b);
+          }
+        }
+        __syncwarp();
+      };
+      if (round > 0 && !wait_ok(&k_empty[st], (round - 1) & 1, abort_flag)) break;
+      copy(&k_full[st], &maps.k, sm + L::kOffK + st * L::kTile);
+      if (round > 0 && !wait_ok(&v_empty[st], (round - 1) & 1, abort_flag)) {
+        tc::mbar_wait(&k_full[st], round & 1);
+        break;
+      }
+      if (PAGED && lane == 0) bad_pages[st] = bad;
+      copy(&v_full[st], &maps.v, sm + L::kOffV + st * L::kTile);
+      issued = i + 1;
+    }
+    // no copy may outlive the block, whatever became of its readers
+    for (int i = max(0, issued - NS); i < issued; ++i) {
+      tc::mbar_wait(&k_full[i % NS], (i / NS) & 1);
+      tc::mbar_wait(&v_full[i % NS], (i / NS) & 1);
+    }
+    for (int t = 0; t < (ntok1 > 0 ? 2 : 1); ++t) tc::mbar_wait(&q_full[t], 0);
+  } else if (warp == kMmaWarp) {
+    // =========================================================================== MMA issuer
+    const bool leader = lane == 0;
+    constexpr uint32_t kIdS = tc::idesc_bf16(kBM, kBN, 0, 0), kIdO = tc::idesc_bf16(kBM, DP, 0, 1);
+    const uint64_t dQ = tc::smem_desc(tc::smem_u32(sm), 16, 1024);
+    const uint64_t dK = tc::smem_desc(tc::smem_u32(sm + L::kOffK), 16, 1024);
+    // V: 64-column blocks 16 KB apart, groups of 8 keys 1 KB apart
+    const uint64_t dV = tc::smem_desc(tc::smem_u32(sm + L::kOffV), kBN * 128, 1024);
+    // K step j (16 columns): 32 bytes inside a 64-column block, then the next block
+    auto kstep = [](int j) -> uint64_t { return (uint64_t)(((j >> 2) * (kBM * 128) + (j & 3) * 32) >> 4); };
+    auto tile_at = [](int i) -> uint64_t { return (uint64_t)((i * L::kTile) >> 4); };
+    int np[2] = {0, 0};
+    bool ok = true;
+    auto scores = [&](int t, int i) {
+      const uint64_t a = dQ + tile_at(t), k = dK + tile_at(i % NS);
+      if (leader) {
+#pragma unroll
+        for (int j = 0; j < DP / 16; ++j) tc::mma_bf16_ss(tb + t * kBN, a + kstep(j), k + kstep(j), kIdS, j > 0);
+        tc::mma_commit(&s_full[t]);
+      }
+      __syncwarp();
+    };
+    auto values = [&](int t, int i) {
+      const uint64_t v = dV + tile_at(i % NS);
+      if (leader) {
+#pragma unroll
+        for (int j = 0; j < kBN / 16; ++j)
+          tc::mma_bf16_ts(tb + 256 + t * DP, tb + t * kBN + 8 * j, v + (uint64_t)(j * 2048 >> 4), kIdO, np[t] > 0 || j > 0);
+      }
+      ++np[t];
+      __syncwarp();
+    };
+    if (n > 0) {
+      for (int t = 0; ok && t < (ntok1 > 0 ? 2 : 1); ++t) ok = wait_ok(&q_full[t], 0, abort_flag);
+      if (ok) ok = wait_ok(&k_full[0], 0, abort_flag);
+      if (ok) {
+        const int tile = walk.tile(w0);
+        for (int t = 0; t < 2; ++t)
+          if (act[t](tile)) scores(t, 0);
+        if (leader) tc::mma_commit(&k_empty[0]);
+        __syncwarp();
+      }
+    }
+    for (int i = 0; ok && i < n; ++i) {
+      const int tile = walk.tile(w0 + i), next = i + 1 < n ? walk.tile(w0 + i + 1) : -1;
+      ok = wait_ok(&v_full[i % NS], (i / NS) & 1, abort_flag);
+      bool have_k = false;
+      for (int t = 0; ok && t < 2; ++t) {
+        if (act[t](tile)) {
+          ok = wait_ok(&p_full[t], np[t] & 1, abort_flag);
+          if (!ok) break;
+          tc::tmem_fence_after();
+          values(t, i);
+        }
+        if (next >= 0 && act[t](next)) {
+          if (!have_k) ok = wait_ok(&k_full[(i + 1) % NS], ((i + 1) / NS) & 1, abort_flag);
+          if (!ok) break;
+          have_k = true;
+          scores(t, i + 1);
+        }
+      }
+      if (!ok) break;
+      if (leader) {
+        tc::mma_commit(&v_empty[i % NS]);
+        if (next >= 0) tc::mma_commit(&k_empty[(i + 1) % NS]);
+      }
+      __syncwarp();
+    }
+    if (leader) {
+      tc::mma_commit(&fin[0]);
+      tc::mma_commit(&fin[1]);
+    }
+    __syncwarp();
+    tc::mbar_wait(&fin[0], 0);  // every MMA issued is done before the block gives up its memory
+  } else {
+    // =========================================================================== rows
+    const int t = warp >> 2;
+    const int r = threadIdx.x & 127;
+    const int ntok = t ? ntok1 : ntok0;
+    const int tok = tok0 + t * tok_tile + r / G;
+    const int pos = s.pos0 + tok;
+    const int pmin = s.pos0 + tok0 + t * tok_tile, pmax = pmin + ntok - 1;
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32);
+    const uint32_t tS = tc::tmem_addr(tb, lane_base, t * kBN), tO = tc::tmem_addr(tb, lane_base, 256 + t * DP);
+    const float scale2 = p.scale * kLog2e;
+    float m = kNegInf, l = 0.f;
+    int done = 0;
+    bool ok = true;
+    for (int i = 0; i < n; ++i) {
+      const int tile = walk.tile(w0 + i);
+      if (!act[t](tile)) continue;
+      const int k0 = tile * kBN;
+      ok = wait_ok(&s_full[t], done & 1, abort_flag);
+      if (!ok) break;
+      tc::tmem_fence_after();
+      uint32_t bad = 0;
+      if (PAGED) {
+        // the list of unusable pages travels with the V tile
+        ok = wait_ok(&v_full[i % NS], (i / NS) & 1, abort_flag);
+        if (!ok) break;
+        bad = *(volatile uint32_t*)&bad_pages[i % NS];
+      }
+      float x[kBN];
+#pragma unroll
+      for (int c = 0; c < kBN; c += 32) tc::tmem_ld32(tS + c, *reinterpret_cast<float(*)[32]>(&x[c]));
+      tc::tmem_wait_ld();
+      const bool whole = k0 + kBN - 1 <= min(pmin, s.kv - 1) &&
+                         (p.window <= 0 || pmax - k0 < p.window || k0 + kBN - 1 < p.sinks) && !bad;
+      if (!whole) {
+        const int hi = min(pos, s.kv - 1) - k0;
+        const int lo = p.window > 0 ? pos - p.window + 1 - k0 : -1;
+        const int sk = p.sinks - k0;
+#pragma unroll
+        for (int c = 0; c < kBN; ++c)
+          if (c > hi || (c < lo && c >= sk)) x[c] = kNegInf;
+        if (bad) {
+          const int rows = min(p.page, kBN);
+#pragma unroll
+          for (int c = 0; c < kBN; ++c)
+            if ((bad >> (c / rows)) & 1) x[c] = kNegInf;
+        }
+        if (PAGED && (k0 + kBN > s.kv || bad)) {
+          // key r of the tile: its V row is cleared where there is no such key
+          const bool hole = k0 + r >= s.kv || ((bad >> (r / min(p.page, kBN))) & 1);
+          if (hole) {
+            unsigned char* v = sm + L::kOffV + (i % NS) * L::kTile + r * 128;
+#pragma unroll
+            for (int c = 0; c < kBlocks; ++c)
+#pragma unroll
+              for (int e = 0; e < 8; ++e) *reinterpret_cast<uint4*>(v + c * (kBN * 128) + e * 16) = make_uint4(0, 0, 0, 0);
+          }
+          tc::fence_async_smem();
+        }
+      }
+      float top = x[0];
+#pragma unroll
+      for (int c = 1; c < kBN; ++c) top = fmaxf(top, x[c]);
+      top *= scale2;
+      if (done == 0) {
+        m = top;
+      } else {
+        const bool move = top > m + kSlack;
+        if (__any_sync(kFull, move)) {
+          // the product that last wrote O was issued before this S: it is done
+          const float f = move ? ex2(m - top) : 1.f;
+          if (move) m = top;
+          l *= f;
+#pragma unroll
+          for (int c = 0; c < DP; c += 32) {
+            float o[32];
+            tc::tmem_ld32(tO + c, o);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] *= f;
+            tc::tmem_st32(tO + c, o);
+          }
+        }
+      }
+      const float ref = m == kNegInf ? 0.f : m;
+      float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float w[32];
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+          const float a = ex2(fmaf(x[64 * h + 2 * c], scale2, -ref)), e = ex2(fmaf(x[64 * h + 2 * c + 1], scale2, -ref));
+          sum0 += a;
+          sum1 += e;
+          w[c] = __uint_as_float(pack_bf16(a, e));
+        }
+        tc::tmem_st32(tS + 32 * h, w);
+      }
+      l += sum0 + sum1;
+      tc::tmem_wait_st();
+      tc::tmem_fence_before();
+      mbar_arrive(&p_full[t]);
+      ++done;
+    }
+    if (ok && done > 0) {
+      ok = wait_ok(&fin[t], 0, abort_flag);
+      tc::tmem_fence_after();
+    }
+    if (ok && ntok > 0) {
+      const bool live = r < ntok * G;
+      const int64_t at = (s.row0 + tok) * p.H + hk * G + r % G;
+      const int64_t total = (int64_t)p.T * (PAGED ? 1 : p.B) * p.H;
+      const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;  // (a NaN stays one)
+#pragma unroll
+      for (int c = 0; c < DP; c += 32) {
+        float o[32];
+        if (done > 0) {
+          tc::tmem_ld32(tO + c, o);
+          tc::tmem_wait_ld();
+        }
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = done > 0 && l != 0.f ? o[e] * inv : 0.f;
+        if (live) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            if (c + e < D) {
+              if (p.splits > 1) {
+                float* to = p.part_o + (split * total + at) * D + c + e;
+                *reinterpret_cast<float4*>(to) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                *reinterpret_cast<float4*>(to + 4) = make_float4(o[e + 4], o[e + 5], o[e + 6], o[e + 7]);
+              } else {
+                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + at * D + c + e) =
+                    make_uint4(pack_bf16(o[e], o[e + 1]), pack_bf16(o[e + 2], o[e + 3]), pack_bf16(o[e + 4], o[e + 5]),
+                               pack_bf16(o[e + 6], o[e + 7]));
+              }
+            }
+          }
+        }
+      }
+      if (live) {
+        const float lse = l == 0.f ? kNegInf : (m + log2f(l)) * kLn2;
+        if (p.splits > 1) p.part_lse[split * total + at] = lse;
+        else if (p.lse) p.lse[at] = lse;
+      }
+    }
+  }
+  tc::tmem_fence_before();
+  __syncthreads();
+  tc::tmem_fence_after();
+  if (warp == kMmaWarp) tc::tmem_dealloc(tb, 512);
+}
+
+int token_tile(const AttnParams& p) { return kBM / p.G; }
+
+int64_t blocks_without_splits(const AttnParams& p) {
+  const int64_t nq = p.table ? p.max_q : p.T;
+  const int64_t per = 2 * token_tile(p);
+  return (nq + per - 1) / per * p.Hkv * p.B;
+}
+
+template <int DP, bool PAGED>
+cudaError_t launch_dp(const Maps& maps, const AttnParams& p, cudaStream_t stream) {
+  cudaError_t e = set_smem_limit<attn_tc_kernel<DP, PAGED>>(Layout<DP>::kBytes);
+  if (e != cudaSuccess) return e;
+  const int64_t blocks = blocks_without_splits(p);
+  if (blocks * p.splits > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  const int npairs = (int)(blocks / ((int64_t)p.Hkv * p.B));
+  attn_tc_kernel<DP, PAGED><<<(unsigned)(blocks * p.splits), kThreads, Layout<DP>::kBytes, stream>>>(maps, p, token_tile(p), npairs);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+bool attn_tc_supported(const AttnParams& p, rsm_dtype dtype) {
+  if (dtype != RSM_BF16 || p.D > 128) return false;
+  if (!p.table) return true;
+  return p.num_pages > 0 && p.table_width > 0 && p.page % 8 == 0 && (kBN % p.page == 0 || p.page % kBN == 0);
+}
+
+// Blocks that share a row's keys: where the rows alone leave SMs idle, as many as fill them once, of at
+// least two key tiles each by the table's width.
+int attn_tc_splits(const AttnParams& p) {
+  if (!p.table) return 1;
+  int64_t keys = (int64_t)p.table_width * p.page;
+  if (p.window > 0) keys = std::min<int64_t>(keys, (int64_t)p.window + p.sinks + p.max_q);
+  const int64_t tiles = (keys + kBN - 1) / kBN;
+  const int64_t want = device_sm_count() / std::max<int64_t>(1, blocks_without_splits(p));
+  return (int)std::max<int64_t>(1, std::min<int64_t>({want, tiles / 2, 64}));
+}
+
+cudaError_t launch_attn_tc(const AttnParams& p, cudaStream_t stream) {
+  Maps maps;
+  const uint64_t D = p.D, H = p.H, Hkv = p.Hkv;
+  const bool paged = p.table != nullptr;
+  const uint64_t T = p.T, B = paged ? 1 : p.B;
+  const int tok = token_tile(p);
+  bool ok = make_map_bf16(&maps.q, p.q, {D, H, T, B}, {D, H * D, T * H * D}, {64, (uint32_t)p.G, (uint32_t)tok, 1});
+  if (paged) {
+    const uint64_t page = p.page, pages = p.num_pages;
+    const uint32_t rows = (uint32_t)std::min(p.page, kBN);
+    for (auto [m, base] : {std::pair<CUtensorMap*, const void*>{&maps.k, p.k}, {&maps.v, p.v}})
+      ok = ok && make_map_bf16(m, base, {D, Hkv, page, pages}, {D, Hkv * D, page * Hkv * D}, {64, 1, rows, 1});
+  } else {
+    for (auto [m, base] : {std::pair<CUtensorMap*, const void*>{&maps.k, p.k}, {&maps.v, p.v}})
+      ok = ok && make_map_bf16(m, base, {D, Hkv, T, B}, {D, Hkv * D, T * Hkv * D}, {64, 1, (uint32_t)kBN, 1});
+  }
+  if (!ok) return cudaErrorInvalidValue;
+  if (p.D <= 64) return paged ? launch_dp<64, true>(maps, p, stream) : launch_dp<64, false>(maps, p, stream);
+  return paged ? launch_dp<128, true>(maps, p, stream) : launch_dp<128, false>(maps, p, stream);
+}
+
+}  // namespace rsm

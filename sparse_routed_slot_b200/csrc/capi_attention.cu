@@ -88,6 +88,11 @@ template <class A> rsm::AttnParams window_params(const A& a) {
   return p;
 }
 
+// bf16 of head dimensions to 128 runs on the tensor cores, everything else in fp32 on CUDA cores.
+cudaError_t launch_forward(const rsm::AttnParams& p, rsm_dtype dtype, cudaStream_t st) {
+  return rsm::attn_tc_supported(p, dtype) ? rsm::launch_attn_tc(p, st) : rsm::launch_attn_simt(p, dtype, st);
+}
+
 template <class A> cudaError_t validate_qkv(const A& a, cudaStream_t st) {
   const int64_t nq = (int64_t)a.B * a.T * a.H * a.D, nk = (int64_t)a.B * a.T * a.Hkv * a.D;
   cudaError_t e = rsm::launch_check_finite(a.q, nq, a.dtype, st);
@@ -153,7 +158,7 @@ rsm::AttnParams paged_params(const rsm_paged_args& a) {
   p.cu_q = a.cu_q; p.kv_len = a.kv_len;
   p.num_pages = a.num_pages; p.page = a.page_size; p.table_width = a.table_width;
   p.max_q = std::min(a.max_q, a.N);
-  p.splits = rsm::attn_simt_splits(p);
+  p.splits = rsm::attn_tc_supported(p, a.dtype) ? rsm::attn_tc_splits(p) : rsm::attn_simt_splits(p);
   return p;
 }
 
@@ -211,7 +216,7 @@ rsm_status rsm_window_forward(const rsm_window_args* a, void* stream) {
     rsm::AttnParams p = window_params(*a);
     p.o = a->o;
     p.lse = a->lse;
-    e = rsm::launch_attn_simt(p, a->dtype, st);
+    e = launch_forward(p, a->dtype, st);
   }
   return finish(e, "rsm_window_forward");
 }
@@ -281,7 +286,7 @@ rsm_status rsm_paged_forward(const rsm_paged_args* a, void* stream) {
   cudaError_t e = a->flags & RSM_FLAG_VALIDATE
                       ? rsm::launch_check_finite(a->q, (int64_t)a->N * a->H * a->D, a->dtype, st)
                       : cudaSuccess;
-  if (e == cudaSuccess) e = rsm::launch_attn_simt(p, a->dtype, st);
+  if (e == cudaSuccess) e = launch_forward(p, a->dtype, st);
   if (e == cudaSuccess && p.splits > 1) e = rsm::launch_attn_combine(p, a->dtype, st);
   return finish(e, "rsm_paged_forward");
 }

@@ -74,6 +74,10 @@ struct AttnParams {
 int attn_simt_splits(const AttnParams& p);
 cudaError_t launch_attn_simt(const AttnParams& p, rsm_dtype dtype, cudaStream_t stream);
 cudaError_t launch_attn_simt_backward(const AttnParams& p, rsm_dtype dtype, cudaStream_t stream);
+// Tensor-core forward (attn_tc.cu): bf16, head dimensions to 128, page sizes that fit its tiles.
+bool attn_tc_supported(const AttnParams& p, rsm_dtype dtype);
+int attn_tc_splits(const AttnParams& p);
+cudaError_t launch_attn_tc(const AttnParams& p, cudaStream_t stream);
 // delta = dO . o for every row (the first step of every backward).
 cudaError_t launch_attn_delta(const AttnParams& p, rsm_dtype dtype, cudaStream_t stream);
 // Joins the partial results of p.splits blocks into o and lse.

@@ -24,9 +24,7 @@
 
 #include <algorithm>
 
-#include "attention.cuh"
-#include "tc.cuh"
-#include "tma_map.h"
+#include "attn_tc.cuh"
 
 namespace rsm {
 
@@ -37,7 +35,6 @@ using namespace attn;
 constexpr int kBM = 128, kBN = 128;
 constexpr int kThreads = 320;
 constexpr int kCopyWarp = 8, kMmaWarp = 9;
-constexpr float kNegInf = -__builtin_inff();
 constexpr float kSlack = 8.f;  // how far (log2) the running maximum may pass the reference
 
 struct Maps {
@@ -52,30 +49,6 @@ template <int DP> struct Layout {
   static constexpr int kBytes = kOffV + kStages * kTile + 1024;
   static_assert(kBytes <= 232448 - 1024, "shared memory budget");
 };
-
-RSM_DEV void mbar_arrive(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(tc::smem_u32(bar)) : "memory");
-}
-
-// Bounded wait of a whole warp. False: the wait expired here or somewhere else in the block.
-RSM_DEV bool wait_ok(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-  if (!tc::mbar_wait(bar, parity)) {
-    *abort_flag = 1;
-    raise_status(RSM_ERR_TIMEOUT);
-  }
-  return !__any_sync(kFull, *abort_flag != 0);
-}
-
-RSM_DEV float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-RSM_DEV uint32_t pack_bf16(float lo, float hi) {
-  const __nv_bfloat162 t = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&t);
-}
 
 // The key tiles that one query tile of the block sees.
 struct Active {

@@ -1,24 +1,27 @@
 // attn_tc.cu -- window and paged attention of bf16 inputs on the 5th-generation tensor cores.
 //
 // One block owns two tiles of 128 packed query rows (token, head of the group) of one key/value head
-// and walks the keys they see in tiles of 128:
+// and walks the keys they see in tiles of 64:
 //   S = Q K^T            tcgen05.mma, both operands from shared memory, fp32 in TMEM
 //   P = 2^(S' - m)       S' = scale log2(e) S; the row's thread reads S from TMEM and writes P back as
 //                        bf16 over the same columns (the softmax weights are rounded here: the second
-//                        product takes bf16, and 2^-9 per weight is below what bf16 outputs keep)
+//                        product takes bf16, and half a step, 2^-9 of a weight, is what the bf16 outputs
+//                        lose anyway)
 //   O += P V             P from TMEM, V as the tile TMA wrote it (contracted over its rows), fp32 in TMEM
-// The reference m of a row moves only when the running maximum has passed it by 2^8, so O is rescaled
-// once or twice per row instead of per tile; sums are of the fp32 weights and stay below 128 * 2^8 a tile.
+// The reference m of a row is its first tile's maximum and moves only when the running one has passed it by
+// 2^32: fp32 sums and bf16 weights keep their relative precision at any scale, so O is next to never
+// rescaled (at 2^8, a warp rescaled every fourth tile of 2048 random keys, at 1600 cycles).
 //
-// Two tiles because they take turns: while one tile's 128 threads do their exponentials, the tensor core
-// multiplies for the other. Per 128 x 128 tile and head dimension 128 the two products take 1024 tensor
-// cycles and the exponentials 1024 of the special function units, so neither leaves room for the other
-// to wait. K and V tiles serve both query tiles.
+// Each query tile has two S buffers, so that S of the next keys is there when the rows' threads finish
+// with this one: the products, not the chain S -> P -> O -> S, set the pace (with one 128-key buffer per
+// tile the chain took 6000 cycles per 128 keys and two query tiles, of which the tensor core was busy
+// 2100). K and V tiles serve both query tiles.
 //
-// Warps: 0-3 and 4-7 the rows of tiles 0 and 1 (a thread per row), 8 copies (TMA), 9 MMA issuer.
-// TMEM columns: S (and P) of the tiles at 0 and 128, O at 256 and 256 + DP.
-// A paged cache is read page by page (page sizes that divide 128 or are multiples of it, from 8 on): a
-// tile is 128 / page copies. Rows of V behind the last key are cleared before P multiplies them, so what
+// Warps: 0-3 and 4-7 the rows of tiles 0 and 1 (a thread per row), 8 copies (TMA), 9 and 10 the MMA issuers
+// of tiles 0 and 1 (a wait in one does not hold the other's products back).
+// TMEM columns: S (and P) buffers of tile t at 128 t and 128 t + 64, O at 256 + t DP.
+// A paged cache is read page by page (page sizes that divide 64 or are multiples of it, from 8 on): a
+// tile is 64 / page copies. Rows of V behind the last key are cleared before P multiplies them, so what
 // the cache holds there does not matter.
 #include <cuda.h>
 
@@ -32,19 +35,19 @@ namespace {
 
 using namespace attn;
 
-constexpr int kBM = 128, kBN = 128;
-constexpr int kThreads = 320;
-constexpr int kCopyWarp = 8, kMmaWarp = 9;
-constexpr float kSlack = 8.f;  // how far (log2) the running maximum may pass the reference
+constexpr int kBM = 128, kBN = 64;
+constexpr int kThreads = 352;
+constexpr int kCopyWarp = 8, kMmaWarp = 9;  // and kMmaWarp + 1
+constexpr float kSlack = 32.f;  // how far (log2) the running maximum may pass the reference
 
 struct Maps {
   CUtensorMap q, k, v;
 };
 
 template <int DP> struct Layout {
-  static constexpr int kStages = DP == 64 ? 4 : 2;
-  static constexpr int kTile = kBM * DP * 2;  // bytes of one operand tile
-  static constexpr int kOffK = 2 * kTile;
+  static constexpr int kStages = 4;
+  static constexpr int kQ = kBM * DP * 2, kTile = kBN * DP * 2;  // bytes of a query and of a key tile
+  static constexpr int kOffK = 2 * kQ;
   static constexpr int kOffV = kOffK + kStages * kTile;
   static constexpr int kBytes = kOffV + kStages * kTile + 1024;
   static_assert(kBytes <= 232448 - 1024, "shared memory budget");
@@ -69,10 +72,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
   constexpr int NS = L::kStages;
   constexpr int kBlocks = DP / 64;  // 64-column blocks of a tile
   extern __shared__ unsigned char smem_raw[];
-  __shared__ uint64_t q_full[2], k_full[NS], k_empty[NS], v_full[NS], v_empty[NS], s_full[2], p_full[2], fin[2];
-  __shared__ uint32_t bad_pages[NS];
+  __shared__ uint64_t q_full[2], k_full[NS], k_empty[NS], v_full[NS], v_empty[NS], s_full[2][2], p_full[2][2], o_done[2],
+      fin[2];
+  __shared__ uint32_t bad_keys[NS];
   __shared__ uint32_t s_tbase;
-  __shared__ int s_abort;
 
   // the last query tiles see the most keys: they start first
   const int split = blockIdx.x % p.splits;
@@ -90,33 +93,32 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
   const Walk walk = key_walk(pos0, pos0 + ntok0 + ntok1 - 1, s.kv, p.window, p.sinks, kBN);
   const int w0 = (int)((int64_t)walk.n * split / p.splits), w1 = (int)((int64_t)walk.n * (split + 1) / p.splits);
   const int n = w1 - w0;
-  Active act[2] = {active_tiles(pos0, pos0 + ntok0 - 1, s.kv, p, true),
-                   active_tiles(pos0 + tok_tile, pos0 + tok_tile + ntok1 - 1, s.kv, p, ntok1 > 0)};
-
+  const int ntiles = ntok1 > 0 ? 2 : 1;  // query tiles
   unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (warp == kMmaWarp) tc::tmem_alloc(&s_tbase, 512);
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&q_full[i], 1);
-      tc::mbar_init(&s_full[i], 1);
-      tc::mbar_init(&p_full[i], kBM);
+      for (int u = 0; u < 2; ++u) {
+        tc::mbar_init(&s_full[i][u], 1);
+        tc::mbar_init(&p_full[i][u], kBM);
+      }
+      tc::mbar_init(&o_done[i], 1);
       tc::mbar_init(&fin[i], 1);
     }
     for (int i = 0; i < NS; ++i) {
       tc::mbar_init(&k_full[i], 1);
-      tc::mbar_init(&k_empty[i], 1);
+      tc::mbar_init(&k_empty[i], ntiles);
       tc::mbar_init(&v_full[i], 1);
-      tc::mbar_init(&v_empty[i], 1);
+      tc::mbar_init(&v_empty[i], ntiles);
     }
     tc::fence_mbar_init();
-    s_abort = 0;
   }
   tc::tmem_fence_before();
   __syncthreads();
   tc::tmem_fence_after();
   const uint32_t tb = s_tbase;
-  volatile int* abort_flag = &s_abort;
 
   if (warp == kCopyWarp) {
     // =========================================================================== copies
@@ -125,11 +127,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       tc::tma_prefetch_desc(&maps.k);
       tc::tma_prefetch_desc(&maps.v);
       const uint32_t qbytes = (uint32_t)(tok_tile * G * 128 * kBlocks);
-      for (int t = 0; t < (ntok1 > 0 ? 2 : 1); ++t) {
+      for (int t = 0; t < ntiles; ++t) {
         tc::mbar_arrive_expect_tx(&q_full[t], qbytes);
         const int64_t tok = (PAGED ? s.row0 : 0) + tok0 + t * tok_tile;
         for (int c = 0; c < kBlocks; ++c)
-          tc::tma_load_4d(sm + t * L::kTile + c * (kBM * 128), &maps.q, &q_full[t], 64 * c, hk * G, (int)tok,
+          tc::tma_load_4d(sm + t * L::kQ + c * (kBM * 128), &maps.q, &q_full[t], 64 * c, hk * G, (int)tok,
                           PAGED ? 0 : b);
       }
     }
@@ -165,13 +167,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         }
         __syncwarp();
       };
-      if (round > 0 && !wait_ok(&k_empty[st], (round - 1) & 1, abort_flag)) break;
+      if (round > 0 && !wait_warp(&k_empty[st], (round - 1) & 1)) break;
       copy(&k_full[st], &maps.k, sm + L::kOffK + st * L::kTile);
-      if (round > 0 && !wait_ok(&v_empty[st], (round - 1) & 1, abort_flag)) {
+      if (round > 0 && !wait_warp(&v_empty[st], (round - 1) & 1)) {
         tc::mbar_wait(&k_full[st], round & 1);
         break;
       }
-      if (PAGED && lane == 0) bad_pages[st] = bad;
+      if (PAGED) {
+        // bit g: the 8 keys from 8 g on stand in an unusable page
+        const uint32_t bits = __ballot_sync(kFull, lane < kBN / 8 && ((bad >> (8 * lane / rows)) & 1));
+        if (lane == 0) bad_keys[st] = bits;
+      }
       copy(&v_full[st], &maps.v, sm + L::kOffV + st * L::kTile);
       issued = i + 1;
     }
@@ -180,132 +186,132 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       tc::mbar_wait(&k_full[i % NS], (i / NS) & 1);
       tc::mbar_wait(&v_full[i % NS], (i / NS) & 1);
     }
-    for (int t = 0; t < (ntok1 > 0 ? 2 : 1); ++t) tc::mbar_wait(&q_full[t], 0);
-  } else if (warp == kMmaWarp) {
-    // =========================================================================== MMA issuer
-    const bool leader = lane == 0;
+    for (int t = 0; t < ntiles; ++t) tc::mbar_wait(&q_full[t], 0);
+  } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
+    // =========================================================================== MMA issuers
+    const int t = warp - kMmaWarp;
     constexpr uint32_t kIdS = tc::idesc_bf16(kBM, kBN, 0, 0), kIdO = tc::idesc_bf16(kBM, DP, 0, 1);
-    const uint64_t dQ = tc::smem_desc(tc::smem_u32(sm), 16, 1024);
+    const uint64_t dQ = tc::smem_desc(tc::smem_u32(sm + t * L::kQ), 16, 1024);
     const uint64_t dK = tc::smem_desc(tc::smem_u32(sm + L::kOffK), 16, 1024);
-    // V: 64-column blocks 16 KB apart, groups of 8 keys 1 KB apart
+    // V: 64-column blocks 8 KB apart, groups of 8 keys 1 KB apart
     const uint64_t dV = tc::smem_desc(tc::smem_u32(sm + L::kOffV), kBN * 128, 1024);
-    // K step j (16 columns): 32 bytes inside a 64-column block, then the next block
-    auto kstep = [](int j) -> uint64_t { return (uint64_t)(((j >> 2) * (kBM * 128) + (j & 3) * 32) >> 4); };
+    // K step j (16 columns) of a tile with R rows: 32 bytes inside a 64-column block, then the next block
+    auto kstep = [](int R, int j) -> uint64_t { return (uint64_t)(((j >> 2) * (R * 128) + (j & 3) * 32) >> 4); };
     auto tile_at = [](int i) -> uint64_t { return (uint64_t)((i * L::kTile) >> 4); };
-    int np[2] = {0, 0};
-    bool ok = true;
-    auto scores = [&](int t, int i) {
-      const uint64_t a = dQ + tile_at(t), k = dK + tile_at(i % NS);
-      if (leader) {
+    const uint32_t cS = tb + t * 128, cO = tb + 256 + t * DP;
+    const Active act = active_tiles(pos0 + t * tok_tile, pos0 + t * tok_tile + (t ? ntok1 : ntok0) - 1, s.kv, p, t < ntiles);
+    if (tc::elect_one()) {
+      int si = 0, ns = 0, np = 0;  // next key tile to score; S and P V products issued
+      bool ok = t < ntiles && n > 0;
+      // S of the next key tile that these rows see, into buffer ns & 1. P of that buffer was multiplied by a
+      // product issued before (one thread's MMAs run in order). A tile that is not seen is let go of once its
+      // copy is there, so that both issuers' releases count for the same round of the stage.
+      auto scores = [&]() {
+        while (si < n) {
+          const int st = si % NS;
+          ok = wait_one(&k_full[st], (si / NS) & 1);
+          if (!ok) return;
+          const bool seen = act(walk.tile(w0 + si));
+          ++si;
+          if (!seen) {
+            mbar_arrive(&k_empty[st]);
+            continue;
+          }
+          const uint64_t k = dK + tile_at(st);
 #pragma unroll
-        for (int j = 0; j < DP / 16; ++j) tc::mma_bf16_ss(tb + t * kBN, a + kstep(j), k + kstep(j), kIdS, j > 0);
-        tc::mma_commit(&s_full[t]);
-      }
-      __syncwarp();
-    };
-    auto values = [&](int t, int i) {
-      const uint64_t v = dV + tile_at(i % NS);
-      if (leader) {
+          for (int j = 0; j < DP / 16; ++j)
+            tc::mma_bf16_ss(cS + (ns & 1) * kBN, dQ + kstep(kBM, j), k + kstep(kBN, j), kIdS, j > 0);
+          tc::mma_commit(&s_full[t][ns & 1]);
+          tc::mma_commit(&k_empty[st]);
+          ++ns;
+          return;
+        }
+      };
+      if (ok) ok = wait_one(&q_full[t], 0);
+      if (ok) scores();
+      if (ok) scores();
+#pragma unroll 1
+      for (int i = 0; ok && i < n; ++i) {
+        const int st = i % NS;
+        ok = wait_one(&v_full[st], (i / NS) & 1);
+        if (!ok) break;
+        if (!act(walk.tile(w0 + i))) {
+          mbar_arrive(&v_empty[st]);
+          continue;
+        }
+        ok = wait_one(&p_full[t][np & 1], (np >> 1) & 1);
+        if (!ok) break;
+        tc::tmem_fence_after();
+        const uint64_t v = dV + tile_at(st);
 #pragma unroll
         for (int j = 0; j < kBN / 16; ++j)
-          tc::mma_bf16_ts(tb + 256 + t * DP, tb + t * kBN + 8 * j, v + (uint64_t)(j * 2048 >> 4), kIdO, np[t] > 0 || j > 0);
+          tc::mma_bf16_ts(cO, cS + (np & 1) * kBN + 8 * j, v + (uint64_t)(j * 2048 >> 4), kIdO, np > 0 || j > 0);
+        tc::mma_commit(&o_done[t]);
+        tc::mma_commit(&v_empty[st]);
+        ++np;
+        scores();
       }
-      ++np[t];
-      __syncwarp();
-    };
-    if (n > 0) {
-      for (int t = 0; ok && t < (ntok1 > 0 ? 2 : 1); ++t) ok = wait_ok(&q_full[t], 0, abort_flag);
-      if (ok) ok = wait_ok(&k_full[0], 0, abort_flag);
-      if (ok) {
-        const int tile = walk.tile(w0);
-        for (int t = 0; t < 2; ++t)
-          if (act[t](tile)) scores(t, 0);
-        if (leader) tc::mma_commit(&k_empty[0]);
-        __syncwarp();
-      }
-    }
-    for (int i = 0; ok && i < n; ++i) {
-      const int tile = walk.tile(w0 + i), next = i + 1 < n ? walk.tile(w0 + i + 1) : -1;
-      ok = wait_ok(&v_full[i % NS], (i / NS) & 1, abort_flag);
-      bool have_k = false;
-      for (int t = 0; ok && t < 2; ++t) {
-        if (act[t](tile)) {
-          ok = wait_ok(&p_full[t], np[t] & 1, abort_flag);
-          if (!ok) break;
-          tc::tmem_fence_after();
-          values(t, i);
-        }
-        if (next >= 0 && act[t](next)) {
-          if (!have_k) ok = wait_ok(&k_full[(i + 1) % NS], ((i + 1) / NS) & 1, abort_flag);
-          if (!ok) break;
-          have_k = true;
-          scores(t, i + 1);
-        }
-      }
-      if (!ok) break;
-      if (leader) {
-        tc::mma_commit(&v_empty[i % NS]);
-        if (next >= 0) tc::mma_commit(&k_empty[(i + 1) % NS]);
-      }
-      __syncwarp();
-    }
-    if (leader) {
-      tc::mma_commit(&fin[0]);
-      tc::mma_commit(&fin[1]);
+      while (ok && si < n) scores();  // tiles behind the last one seen
+      tc::mma_commit(&fin[t]);
     }
     __syncwarp();
-    tc::mbar_wait(&fin[0], 0);  // every MMA issued is done before the block gives up its memory
-  } else {
+    tc::mbar_wait(&fin[t], 0);  // every MMA issued is done before the block gives up its memory
+  } else if (warp < kCopyWarp) {
     // =========================================================================== rows
     const int t = warp >> 2;
     const int r = threadIdx.x & 127;
     const int ntok = t ? ntok1 : ntok0;
+    const Active act = active_tiles(pos0 + t * tok_tile, pos0 + t * tok_tile + ntok - 1, s.kv, p, ntok > 0);
     const int tok = tok0 + t * tok_tile + r / G;
     const int pos = s.pos0 + tok;
     const int pmin = s.pos0 + tok0 + t * tok_tile, pmax = pmin + ntok - 1;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32);
-    const uint32_t tS = tc::tmem_addr(tb, lane_base, t * kBN), tO = tc::tmem_addr(tb, lane_base, 256 + t * DP);
+    const uint32_t tS = tc::tmem_addr(tb, lane_base, t * 128), tO = tc::tmem_addr(tb, lane_base, 256 + t * DP);
     const float scale2 = p.scale * kLog2e;
     float m = kNegInf, l = 0.f;
     int done = 0;
     bool ok = true;
+#pragma unroll 1
     for (int i = 0; i < n; ++i) {
       const int tile = walk.tile(w0 + i);
-      if (!act[t](tile)) continue;
+      if (!act(tile)) continue;
       const int k0 = tile * kBN;
-      ok = wait_ok(&s_full[t], done & 1, abort_flag);
+      ok = wait_warp(&s_full[t][done & 1], (done >> 1) & 1);
       if (!ok) break;
       tc::tmem_fence_after();
+      const uint32_t tSi = tS + (done & 1) * kBN;
+      float x[kBN];
+      tc::tmem_ld32(tSi, *reinterpret_cast<float(*)[32]>(&x[0]));
+      tc::tmem_ld32(tSi + 32, *reinterpret_cast<float(*)[32]>(&x[32]));
       uint32_t bad = 0;
       if (PAGED) {
         // the list of unusable pages travels with the V tile
-        ok = wait_ok(&v_full[i % NS], (i / NS) & 1, abort_flag);
+        ok = wait_warp(&v_full[i % NS], (i / NS) & 1);
         if (!ok) break;
-        bad = *(volatile uint32_t*)&bad_pages[i % NS];
+        bad = *(volatile uint32_t*)&bad_keys[i % NS];
       }
-      float x[kBN];
-#pragma unroll
-      for (int c = 0; c < kBN; c += 32) tc::tmem_ld32(tS + c, *reinterpret_cast<float(*)[32]>(&x[c]));
       tc::tmem_wait_ld();
       const bool whole = k0 + kBN - 1 <= min(pmin, s.kv - 1) &&
                          (p.window <= 0 || pmax - k0 < p.window || k0 + kBN - 1 < p.sinks) && !bad;
       if (!whole) {
+        // columns [0, sk) and [lo, hi] are seen
         const int hi = min(pos, s.kv - 1) - k0;
-        const int lo = p.window > 0 ? pos - p.window + 1 - k0 : -1;
-        const int sk = p.sinks - k0;
+        const int lo = p.window > 0 ? pos - p.window + 1 - k0 : 0;
+        const int sk = min(p.sinks - k0, hi + 1);
 #pragma unroll
-        for (int c = 0; c < kBN; ++c)
-          if (c > hi || (c < lo && c >= sk)) x[c] = kNegInf;
-        if (bad) {
-          const int rows = min(p.page, kBN);
+        for (int c = 0; c < kBN; c += 32) {
+          uint32_t w = (below(hi + 1 - c) & ~below(lo - c)) | below(sk - c);
+          if (PAGED) {
+            const uint32_t g = bad >> (c / 8);
+            w &= ~((g & 1 ? 0xffu : 0u) | (g & 2 ? 0xff00u : 0u) | (g & 4 ? 0xff0000u : 0u) | (g & 8 ? 0xff000000u : 0u));
+          }
 #pragma unroll
-          for (int c = 0; c < kBN; ++c)
-            if ((bad >> (c / rows)) & 1) x[c] = kNegInf;
+          for (int e = 0; e < 32; ++e)
+            if (!(w & (1u << e))) x[c + e] = kNegInf;
         }
         if (PAGED && (k0 + kBN > s.kv || bad)) {
           // key r of the tile: its V row is cleared where there is no such key
-          const bool hole = k0 + r >= s.kv || ((bad >> (r / min(p.page, kBN))) & 1);
-          if (hole) {
+          if (r < kBN && (k0 + r >= s.kv || ((bad >> (r / 8)) & 1))) {
             unsigned char* v = sm + L::kOffV + (i % NS) * L::kTile + r * 128;
 #pragma unroll
             for (int c = 0; c < kBlocks; ++c)
@@ -315,20 +321,28 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
           tc::fence_async_smem();
         }
       }
-      float top = x[0];
+      float top4[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-      for (int c = 1; c < kBN; ++c) top = fmaxf(top, x[c]);
-      top *= scale2;
+      for (int c = 4; c < kBN - 4; c += 8)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top4[e] = max3(top4[e], x[c + e], x[c + e + 4]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) top4[e] = fmaxf(top4[e], x[kBN - 4 + e]);
+      const float top = fmaxf(max3(top4[0], top4[1], top4[2]), top4[3]) * scale2;
       if (done == 0) {
         m = top;
       } else {
         const bool move = top > m + kSlack;
-        if (__any_sync(kFull, move)) {
-          // the product that last wrote O was issued before this S: it is done
+        // (a row that has seen nothing yet has nothing to rescale)
+        if (__any_sync(kFull, move && m != kNegInf)) {
+          // O is this warp's once the last product into it is done (the one before was when this S came, and
+          // the next waits for this warp: the parity names one phase)
+          ok = wait_warp(&o_done[t], (done - 1) & 1);
+          if (!ok) break;
+          tc::tmem_fence_after();
           const float f = move ? ex2(m - top) : 1.f;
-          if (move) m = top;
           l *= f;
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < DP; c += 32) {
             float o[32];
             tc::tmem_ld32(tO + c, o);
@@ -338,29 +352,33 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             tc::tmem_st32(tO + c, o);
           }
         }
+        if (move) m = top;
       }
       const float ref = m == kNegInf ? 0.f : m;
-      float sum0 = 0.f, sum1 = 0.f;
+      const float2 s2 = make_float2(scale2, scale2), r2 = make_float2(-ref, -ref);
+      float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        float w[32];
+        float w[16];
 #pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          const float a = ex2(fmaf(x[64 * h + 2 * c], scale2, -ref)), e = ex2(fmaf(x[64 * h + 2 * c + 1], scale2, -ref));
-          sum0 += a;
-          sum1 += e;
-          w[c] = __uint_as_float(pack_bf16(a, e));
+        for (int c = 0; c < 16; ++c) {
+          float2 e = fma2(make_float2(x[32 * h + 2 * c], x[32 * h + 2 * c + 1]), s2, r2);
+          e.x = ex2(e.x);
+          e.y = ex2(e.y);
+          if (c & 1) sum1 = add2(sum1, e);
+          else sum0 = add2(sum0, e);
+          w[c] = __uint_as_float(pack_bf16(e.x, e.y));
         }
-        tc::tmem_st32(tS + 32 * h, w);
+        tc::tmem_st16(tSi + 16 * h, w);
       }
-      l += sum0 + sum1;
+      l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
       tc::tmem_wait_st();
       tc::tmem_fence_before();
-      mbar_arrive(&p_full[t]);
+      mbar_arrive(&p_full[t][done & 1]);
       ++done;
     }
     if (ok && done > 0) {
-      ok = wait_ok(&fin[t], 0, abort_flag);
+      ok = wait_warp(&fin[t], 0);
       tc::tmem_fence_after();
     }
     if (ok && ntok > 0) {
@@ -368,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       const int64_t at = (s.row0 + tok) * p.H + hk * G + r % G;
       const int64_t total = (int64_t)p.T * (PAGED ? 1 : p.B) * p.H;
       const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;  // (a NaN stays one)
-#pragma unroll
+#pragma unroll 1
       for (int c = 0; c < DP; c += 32) {
         float o[32];
         if (done > 0) {
@@ -435,14 +453,14 @@ bool attn_tc_supported(const AttnParams& p, rsm_dtype dtype) {
 }
 
 // Blocks that share a row's keys: where the rows alone leave SMs idle, as many as fill them once, of at
-// least two key tiles each by the table's width.
+// least four key tiles each by the table's width.
 int attn_tc_splits(const AttnParams& p) {
   if (!p.table) return 1;
   int64_t keys = (int64_t)p.table_width * p.page;
   if (p.window > 0) keys = std::min<int64_t>(keys, (int64_t)p.window + p.sinks + p.max_q);
   const int64_t tiles = (keys + kBN - 1) / kBN;
   const int64_t want = device_sm_count() / std::max<int64_t>(1, blocks_without_splits(p));
-  return (int)std::max<int64_t>(1, std::min<int64_t>({want, tiles / 2, 64}));
+  return (int)std::max<int64_t>(1, std::min<int64_t>({want, tiles / 4, 64}));
 }
 
 cudaError_t launch_attn_tc(const AttnParams& p, cudaStream_t stream) {

@@ -16,19 +16,46 @@ RSM_DEV void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(tc::smem_u32(bar)) : "memory");
 }
 
-// Bounded wait of a whole warp. False: the wait expired here or somewhere else in the block.
-RSM_DEV bool wait_ok(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-  if (!tc::mbar_wait(bar, parity)) {
-    *abort_flag = 1;
-    raise_status(RSM_ERR_TIMEOUT);
-  }
-  return !__any_sync(kFull, *abort_flag != 0);
+// Bounded waits. An expired wait is reported, and its warp stops; every other role of the block depends on
+// some wait that then expires as well. (A shared flag read beside each wait would cost a third of it.)
+RSM_DEV bool wait_one(uint64_t* bar, uint32_t parity) {
+  if (tc::mbar_wait(bar, parity)) return true;
+  raise_status(RSM_ERR_TIMEOUT);
+  return false;
 }
+// The same decision in every lane of a warp.
+RSM_DEV bool wait_warp(uint64_t* bar, uint32_t parity) { return __all_sync(kFull, wait_one(bar, parity)); }
+
+// The lowest n bits of a word (n below 0: none, above 32: all).
+RSM_DEV uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
 
 RSM_DEV float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// Two fp32 operations in one instruction, and the largest of three.
+RSM_DEV float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\tmov.b64 rc, {%6, %7};\n\t"
+      "fma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+RSM_DEV float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+      "add.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+RSM_DEV float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 
 RSM_DEV uint32_t pack_bf16(float lo, float hi) {

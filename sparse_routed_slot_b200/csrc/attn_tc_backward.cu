@@ -125,7 +125,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_dkv_kernel(const __grid_c
       ds_full, fin;
   __shared__ __align__(16) float stat[2][2][kBM];  // per stage: lse (base 2) and delta of the rows
   __shared__ uint32_t s_tbase;
-  __shared__ int s_abort;
 
   // Blocks of the first key tiles, whose walks are longest, start first; behind them the far chunks.
   const int pairs = p.Hkv * p.B;
@@ -175,7 +174,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_dkv_kernel(const __grid_c
     tc::mbar_init(&ds_full, kRowThreads);
     tc::mbar_init(&fin, 1);
     tc::fence_mbar_init();
-    s_abort = 0;
   }
   if (rows_tile < kBM) {
     for (int i = 0; i < 2; ++i) {
@@ -189,7 +187,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_dkv_kernel(const __grid_c
   tc::tmem_fence_after();
   const uint32_t tb = s_tbase;
   const uint32_t cS = tb, cP = tb + 128, cV = tb + 256, cK = tb + 256 + DP;
-  volatile int* abort_flag = &s_abort;
 
   if (warp == kCopyWarp) {
     // =========================================================================== copies
@@ -212,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_dkv_kernel(const __grid_c
         }
         __syncwarp();
       };
-      if (round > 0 && !wait_ok(&q_empty[st], (round - 1) & 1, abort_flag)) break;
+      if (round > 0 && !wait_warp(&q_empty[st], (round - 1) & 1)) break;
       copy(&q_full[st], &maps.q, sQ + st * L::kTile);
       nq = i + 1;
       // the stage's statistics were last read for a dS that the emptied Q tile's product used
@@ -232,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_dkv_kernel(const __grid_c
       }
       mbar_arrive(&st_full[st]);
       __syncwarp();
-      if (round > 0 && !wait_ok(&do_empty[st], (round - 1) & 1, abort_flag)) break;
+      if (round > 0 && !wait_warp(&do_empty[st], (round - 1) & 1)) break;
       copy(&do_full[st], &maps.dO, sO + st * L::kTile);
       ndo = i + 1;
     }
@@ -242,57 +239,45 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_dkv_kernel(const __grid_c
     for (int i = max(0, ndo - 2); i < ndo; ++i) tc::mbar_wait(&do_full[i & 1], (i >> 1) & 1);
   } else if (warp == kMmaWarp) {
     // =========================================================================== MMA issuer
-    const bool leader = lane == 0;
     const uint64_t dK = tc::smem_desc(tc::smem_u32(sK), 16, 1024), dV = tc::smem_desc(tc::smem_u32(sV), 16, 1024);
     const uint64_t dQ = tc::smem_desc(tc::smem_u32(sQ), 16, 1024), dO = tc::smem_desc(tc::smem_u32(sO), 16, 1024);
     const uint64_t rQ = tc::smem_desc(tc::smem_u32(sQ), kBM * 128, 1024), rO = tc::smem_desc(tc::smem_u32(sO), kBM * 128, 1024);
     auto stage = [](int i) -> uint64_t { return (uint64_t)(((i & 1) * L::kTile) >> 4); };
-    auto scores = [&](int i) {
-      if (leader) {
+    if (tc::elect_one()) {
+      auto scores = [&](int i) {
         product_ss<DP>(cS, dK, dQ + stage(i));
         tc::mma_commit(&s_full);
-      }
-      __syncwarp();
-    };
-    auto dprobs = [&](int i) {
-      if (leader) {
+      };
+      auto dprobs = [&](int i) {
         product_ss<DP>(cP, dV, dO + stage(i));
         tc::mma_commit(&dp_full);
+      };
+      bool ok = n > 0 && wait_one(&kv_full, 0) && wait_one(&q_full[0], 0);
+      if (ok) {
+        scores(0);
+        ok = wait_one(&do_full[0], 0);
+        if (ok) dprobs(0);
       }
-      __syncwarp();
-    };
-    bool ok = n > 0 && wait_ok(&kv_full, 0, abort_flag) && wait_ok(&q_full[0], 0, abort_flag);
-    if (ok) {
-      scores(0);
-      ok = wait_ok(&do_full[0], 0, abort_flag);
-      if (ok) dprobs(0);
-    }
-    for (int i = 0; ok && i < n; ++i) {
-      const int nx = i + 1;
-      if (!(ok = wait_ok(&p_full, i & 1, abort_flag))) break;
-      tc::tmem_fence_after();
-      if (leader) {
+#pragma unroll 1
+      for (int i = 0; ok && i < n; ++i) {
+        const int nx = i + 1;
+        if (nx < n && !(ok = wait_one(&q_full[nx & 1], (nx >> 1) & 1))) break;
+        if (!(ok = wait_one(&p_full, i & 1))) break;
+        tc::tmem_fence_after();
         product_ts<DP>(cV, cS, rO + stage(i), i > 0);
         tc::mma_commit(&do_empty[i & 1]);
-      }
-      __syncwarp();
-      if (nx < n) {
-        if (!(ok = wait_ok(&q_full[nx & 1], (nx >> 1) & 1, abort_flag))) break;
-        scores(nx);
-      }
-      if (!(ok = wait_ok(&ds_full, i & 1, abort_flag))) break;
-      tc::tmem_fence_after();
-      if (leader) {
+        if (nx < n) {
+          scores(nx);
+          if (!(ok = wait_one(&do_full[nx & 1], (nx >> 1) & 1))) break;
+        }
+        if (!(ok = wait_one(&ds_full, i & 1))) break;
+        tc::tmem_fence_after();
         product_ts<DP>(cK, cP, rQ + stage(i), i > 0);
         tc::mma_commit(&q_empty[i & 1]);
+        if (nx < n) dprobs(nx);
       }
-      __syncwarp();
-      if (nx < n) {
-        if (!(ok = wait_ok(&do_full[nx & 1], (nx >> 1) & 1, abort_flag))) break;
-        dprobs(nx);
-      }
+      tc::mma_commit(&fin);
     }
-    if (leader) tc::mma_commit(&fin);
     __syncwarp();
     tc::mbar_wait(&fin, 0);  // every MMA issued is done before the block gives up its memory
   } else {
@@ -314,8 +299,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_dkv_kernel(const __grid_c
       const bool whole = __all_sync(kFull, lo <= 0 && hi >= 64);
       const float4* sl = reinterpret_cast<const float4*>(&stat[i & 1][0][64 * half]);
       const float4* sd = reinterpret_cast<const float4*>(&stat[i & 1][1][64 * half]);
-      if (!(ok = wait_ok(&st_full[i & 1], (i >> 1) & 1, abort_flag))) break;
-      if (!(ok = wait_ok(&s_full, i & 1, abort_flag))) break;
+      if (!(ok = wait_warp(&st_full[i & 1], (i >> 1) & 1))) break;
+      if (!(ok = wait_warp(&s_full, i & 1))) break;
       tc::tmem_fence_after();
       float x[64];
       tc::tmem_ld32(tS, *reinterpret_cast<float(*)[32]>(&x[0]));
@@ -343,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_dkv_kernel(const __grid_c
       tc::tmem_wait_st();
       tc::tmem_fence_before();
       mbar_arrive(&p_full);
-      if (!(ok = wait_ok(&dp_full, i & 1, abort_flag))) break;
+      if (!(ok = wait_warp(&dp_full, i & 1))) break;
       tc::tmem_fence_after();
       float w[32];
 #pragma unroll
@@ -365,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_dkv_kernel(const __grid_c
       tc::tmem_fence_before();
       mbar_arrive(&ds_full);
     }
-    if (ok) ok = wait_ok(&fin, 0, abort_flag);
+    if (ok) ok = wait_warp(&fin, 0);
     if (ok) {
       tc::tmem_fence_after();
       const uint32_t src = tc::tmem_addr(half ? cK : cV, lane_base, 0);
@@ -432,7 +417,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_dq_kernel(const __grid_co
   extern __shared__ unsigned char smem_raw[];
   __shared__ uint64_t q_full, k_full[3], k_empty[3], v_full[2], v_empty[2], s_full[2], dp_full, ds_full, fin;
   __shared__ uint32_t s_tbase;
-  __shared__ int s_abort;
 
   const int tile = ntiles - 1 - blockIdx.x % ntiles;  // the last tiles see the most keys: they start first
   const int pair = blockIdx.x / ntiles;
@@ -462,14 +446,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_dq_kernel(const __grid_co
     tc::mbar_init(&ds_full, kRowThreads);
     tc::mbar_init(&fin, 1);
     tc::fence_mbar_init();
-    s_abort = 0;
   }
   tc::tmem_fence_before();
   __syncthreads();
   tc::tmem_fence_after();
   const uint32_t tb = s_tbase;
   const uint32_t cS = tb, cP = tb + 256, cQ = tb + 384;  // S at 0 and 128
-  volatile int* abort_flag = &s_abort;
 
   if (warp == kCopyWarp) {
     // =========================================================================== copies
@@ -491,10 +473,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_dq_kernel(const __grid_co
         }
         __syncwarp();
       };
-      if (i >= 3 && !wait_ok(&k_empty[i % 3], (i / 3 - 1) & 1, abort_flag)) break;
+      if (i >= 3 && !wait_warp(&k_empty[i % 3], (i / 3 - 1) & 1)) break;
       copy(&k_full[i % 3], &maps.k, sK + (i % 3) * L::kTile);
       nk = i + 1;
-      if (i >= 2 && !wait_ok(&v_empty[i & 1], ((i >> 1) - 1) & 1, abort_flag)) break;
+      if (i >= 2 && !wait_warp(&v_empty[i & 1], ((i >> 1) - 1) & 1)) break;
       copy(&v_full[i & 1], &maps.v, sV + (i & 1) * L::kTile);
       nv = i + 1;
     }
@@ -504,46 +486,39 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_dq_kernel(const __grid_co
     for (int i = max(0, nv - 2); i < nv; ++i) tc::mbar_wait(&v_full[i & 1], (i >> 1) & 1);
   } else if (warp == kMmaWarp) {
     // =========================================================================== MMA issuer
-    const bool leader = lane == 0;
     const uint64_t dQ = tc::smem_desc(tc::smem_u32(sQ), 16, 1024), dO = tc::smem_desc(tc::smem_u32(sO), 16, 1024);
     const uint64_t dK = tc::smem_desc(tc::smem_u32(sK), 16, 1024), dV = tc::smem_desc(tc::smem_u32(sV), 16, 1024);
     const uint64_t rK = tc::smem_desc(tc::smem_u32(sK), kBN * 128, 1024);
     auto at = [](int i) -> uint64_t { return (uint64_t)((i * L::kTile) >> 4); };
-    bool ok = wait_ok(&q_full, 0, abort_flag);
-    auto scores = [&](int i) {
-      ok = ok && wait_ok(&k_full[i % 3], (i / 3) & 1, abort_flag);
-      if (ok && leader) {
+    if (tc::elect_one()) {
+      bool ok = wait_one(&q_full, 0);
+      auto scores = [&](int i) {
+        ok = ok && wait_one(&k_full[i % 3], (i / 3) & 1);
+        if (!ok) return;
         product_ss<DP>(cS + (i & 1) * 128, dQ, dK + at(i % 3));
         tc::mma_commit(&s_full[i & 1]);
-      }
-      __syncwarp();
-    };
-    auto dprobs = [&](int i) {
-      ok = ok && wait_ok(&v_full[i & 1], (i >> 1) & 1, abort_flag);
-      if (ok && leader) {
+      };
+      auto dprobs = [&](int i) {
         product_ss<DP>(cP, dO, dV + at(i & 1));
         tc::mma_commit(&dp_full);
         tc::mma_commit(&v_empty[i & 1]);
-      }
-      __syncwarp();
-    };
-    scores(0);
-    dprobs(0);
-    if (n > 1) scores(1);
-    for (int i = 0; ok && i < n; ++i) {
-      ok = wait_ok(&ds_full, i & 1, abort_flag);
-      if (!ok) break;
-      tc::tmem_fence_after();
-      if (i + 1 < n) dprobs(i + 1);
-      if (!ok) break;
-      if (leader) {
+      };
+      scores(0);
+      ok = ok && wait_one(&v_full[0], 0);
+      if (ok) dprobs(0);
+      if (n > 1) scores(1);
+#pragma unroll 1
+      for (int i = 0; ok && i < n; ++i) {
+        if (i + 1 < n && !(ok = wait_one(&v_full[(i + 1) & 1], ((i + 1) >> 1) & 1))) break;
+        if (!(ok = wait_one(&ds_full, i & 1))) break;
+        tc::tmem_fence_after();
+        if (i + 1 < n) dprobs(i + 1);
         product_ts<DP>(cQ, cS + (i & 1) * 128, rK + at(i % 3), i > 0);
         tc::mma_commit(&k_empty[i % 3]);
+        if (i + 2 < n) scores(i + 2);
       }
-      __syncwarp();
-      if (i + 2 < n) scores(i + 2);
+      tc::mma_commit(&fin);
     }
-    if (leader) tc::mma_commit(&fin);
     __syncwarp();
     tc::mbar_wait(&fin, 0);  // every MMA issued is done before the block gives up its memory
   } else {
@@ -560,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_dq_kernel(const __grid_co
     bool ok = true;
     for (int i = 0; i < n; ++i) {
       const int k0 = walk.tile(i) * kBN + 64 * half;
-      if (!(ok = wait_ok(&s_full[i & 1], (i >> 1) & 1, abort_flag))) break;
+      if (!(ok = wait_warp(&s_full[i & 1], (i >> 1) & 1))) break;
       tc::tmem_fence_after();
       const uint32_t tSi = tS + (i & 1) * 128;
       float x[64];
@@ -576,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_dq_kernel(const __grid_co
         for (int c = 0; c < 64; ++c)
           if (c > hi || (c < lo && c >= sk)) x[c] = 0.f;
       }
-      if (!(ok = wait_ok(&dp_full, i & 1, abort_flag))) break;
+      if (!(ok = wait_warp(&dp_full, i & 1))) break;
       tc::tmem_fence_after();
       float w[32];
 #pragma unroll
@@ -594,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_dq_kernel(const __grid_co
       tc::tmem_fence_before();
       mbar_arrive(&ds_full);
     }
-    if (ok) ok = wait_ok(&fin, 0, abort_flag);
+    if (ok) ok = wait_warp(&fin, 0);
     if (ok) {
       tc::tmem_fence_after();
       constexpr int kHalf = DP / 2;

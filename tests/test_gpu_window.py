@@ -34,7 +34,8 @@ SHAPES = [(1, 1, 1, 1, 64, 1, 0), (2, 2, 2, 1, 8, 1, 0), (1, 5, 3, 1, 16, 2, 1),
           (1, 65, 6, 2, 64, 33, 5), (2, 127, 4, 1, 128, 16, 37), (1, 128, 2, 2, 128, 128, 0), (1, 129, 5, 1, 80, 128, 3),
           (1, 257, 8, 8, 128, 100, 130), (1, 300, 6, 2, 72, 1000, 0), (2, 400, 7, 1, 64, 127, 4), (1, 513, 3, 3, 96, 256, 1),
           (1, 700, 4, 2, 120, 65, 300), (1, 1025, 2, 1, 128, 511, 64), (1, 260, 2, 1, 256, 90, 2), (1, 200, 3, 3, 136, 300, 9),
-          (1, 130, 64, 1, 64, 40, 2), (1, 1500, 2, 2, 128, 1, 1), (3, 333, 4, 2, 64, 200, 500)]
+          (1, 130, 64, 1, 64, 40, 2), (1, 1500, 2, 2, 128, 1, 1), (3, 333, 4, 2, 64, 200, 500),
+          (1, 2048, 2, 2, 128, 512, 4), (1, 5400, 1, 1, 64, 100, 140), (1, 4200, 3, 1, 128, 300, 5), (1, 1900, 2, 2, 80, 2000, 0)]
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])

@@ -15,7 +15,11 @@
 // Each query tile has two S buffers, so that S of the next keys is there when the rows' threads finish
 // with this one: the products, not the chain S -> P -> O -> S, set the pace (with one 128-key buffer per
 // tile the chain took 6000 cycles per 128 keys and two query tiles, of which the tensor core was busy
-// 2100). K and V tiles serve both query tiles.
+// 2100). The two warps of a scheduler, one of each query tile, take turns at their exponentials: left
+// alone they fall into step, and the special function units idle while both load and look for maxima.
+// A step of 64 keys and two query tiles needs 1024 cycles of the special function units and 1280 of the
+// tensor core (S of 64 keys runs at 3/4 rate, bound by its operands from shared memory) and takes 1750.
+// K and V tiles serve both query tiles.
 //
 // Warps: 0-3 and 4-7 the rows of tiles 0 and 1 (a thread per row), 8 copies (TMA), 9 and 10 the MMA issuers
 // of tiles 0 and 1 (a wait in one does not hold the other's products back).
@@ -53,17 +57,31 @@ template <int DP> struct Layout {
   static_assert(kBytes <= 232448 - 1024, "shared memory budget");
 };
 
-// The key tiles that one query tile of the block sees.
-struct Active {
-  int ns, first, last;
-  RSM_DEV bool operator()(int tile) const { return tile <= last && (tile < ns || tile >= first); }
+// The steps of the block's walk [w0, w0 + n) in which one query tile sees the keys: [0, sinks) and [first, end).
+struct Steps {
+  int sinks, first, end;
+  RSM_DEV bool operator()(int i) const { return i < end && (i >= first || i < sinks); }
+  RSM_DEV int count(int n) const {
+    int c = 0;
+    for (int i = 0; i < n; ++i) c += (*this)(i);
+    return c;
+  }
 };
 
-RSM_DEV Active active_tiles(int p0, int p1, int kv, const AttnParams& p, bool any) {
+RSM_DEV Steps steps_of(const Walk& all, int w0, int n, int p0, int p1, int kv, const AttnParams& p, bool any) {
   const Walk w = key_walk(p0, p1, kv, p.window, p.sinks, kBN);
-  if (!any || w.n == 0) return {0, 0, -1};
-  return {w.ns, w.first, w.n > w.ns ? w.first + (w.n - w.ns) - 1 : w.ns - 1};
+  if (!any || w.n == 0) return {0, 0, 0};
+  // step of the block's walk that has key tile x (the tiles of a query tile are tiles of the block)
+  auto step = [&](int x) { return (x < all.ns ? x : all.ns + (x - all.first)) - w0; };
+  Steps s;
+  s.sinks = min(w.ns - w0, n);
+  s.first = w.n > w.ns ? step(w.first) : n;
+  s.end = min(n, w.n > w.ns ? step(w.first + (w.n - w.ns) - 1) + 1 : w.ns - w0);
+  return s;
 }
+
+RSM_DEV void turn_wait(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
+RSM_DEV void turn_pass(int id) { asm volatile("bar.arrive %0, 64;" ::"r"(id) : "memory"); }
 
 template <int DP, bool PAGED>
 __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_constant__ Maps maps, const AttnParams p,
@@ -72,7 +90,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
   constexpr int NS = L::kStages;
   constexpr int kBlocks = DP / 64;  // 64-column blocks of a tile
   extern __shared__ unsigned char smem_raw[];
-  __shared__ uint64_t q_full[2], k_full[NS], k_empty[NS], v_full[NS], v_empty[NS], s_full[2][2], p_full[2][2], o_done[2],
+  __shared__ uint64_t q_full[2], full[NS], empty[NS], s_full[2][2], p_full[2][2],
       fin[2];
   __shared__ uint32_t bad_keys[NS];
   __shared__ uint32_t s_tbase;
@@ -102,16 +120,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       tc::mbar_init(&q_full[i], 1);
       for (int u = 0; u < 2; ++u) {
         tc::mbar_init(&s_full[i][u], 1);
-        tc::mbar_init(&p_full[i][u], kBM);
+        tc::mbar_init(&p_full[i][u], 4);
       }
-      tc::mbar_init(&o_done[i], 1);
       tc::mbar_init(&fin[i], 1);
     }
     for (int i = 0; i < NS; ++i) {
-      tc::mbar_init(&k_full[i], 1);
-      tc::mbar_init(&k_empty[i], ntiles);
-      tc::mbar_init(&v_full[i], 1);
-      tc::mbar_init(&v_empty[i], ntiles);
+      tc::mbar_init(&full[i], 1);
+      tc::mbar_init(&empty[i], ntiles);
     }
     tc::fence_mbar_init();
   }
@@ -136,56 +151,56 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       }
     }
     __syncwarp();
-    int issued = 0;  // K tiles whose copies were started (V follows its K)
-    for (int i = 0; i < n; ++i) {
-      const int st = i % NS, round = i / NS;
-      const int k0 = walk.tile(w0 + i) * kBN;
-      int page_id = 0;
-      uint32_t wanted = 1, bad = 0;
-      const int rows = PAGED ? min(p.page, kBN) : kBN;  // rows of one copy
-      if (PAGED) {
-        // lane l fetches page l of the tile
-        const int key = k0 + lane * rows;
+    // Unit c of the ring: K of step c and V of step c - 2, which the issuers take up together.
+    const int rows = PAGED ? min(p.page, kBN) : kBN;  // rows of one copy
+    int page_id[3] = {0, 0, 0};                       // lane l: page l of the tiles of steps c, c - 1 and c - 2
+    uint32_t wanted[3] = {0, 0, 0}, bad[3] = {0, 0, 0};
+    int issued = 0;
+#pragma unroll 1
+    for (int c = 0; c < n + 2; ++c) {
+      const int st = c % NS;
+      page_id[2] = page_id[1]; page_id[1] = page_id[0];
+      wanted[2] = wanted[1]; wanted[1] = wanted[0];
+      bad[2] = bad[1]; bad[1] = bad[0];
+      wanted[0] = c < n ? 1 : 0;
+      if (PAGED && c < n) {
+        const int key = walk.tile(w0 + c) * kBN + lane * rows;
         const bool in = lane * rows < kBN && key < s.kv;
-        if (in) page_id = p.table[(int64_t)b * p.table_width + key / p.page];
-        const bool ok = in && (unsigned)page_id < (unsigned)p.num_pages;
-        wanted = __ballot_sync(kFull, ok);
-        bad = __ballot_sync(kFull, in && !ok);
-        if (bad && lane == 0) raise_status(RSM_ERR_BAD_PAGE);
+        if (in) page_id[0] = p.table[(int64_t)b * p.table_width + key / p.page];
+        const bool usable = in && (unsigned)page_id[0] < (unsigned)p.num_pages;
+        wanted[0] = __ballot_sync(kFull, usable);
+        bad[0] = __ballot_sync(kFull, in && !usable);
+        if (bad[0] && lane == 0) raise_status(RSM_ERR_BAD_PAGE);
       }
-      auto copy = [&](uint64_t* full, const CUtensorMap* map, unsigned char* dst) {
-        if (lane == 0) tc::mbar_arrive_expect_tx(full, (uint32_t)__popc(wanted) * rows * 128 * kBlocks);
-        __syncwarp();
-        if ((wanted >> lane) & 1) {
-          for (int c = 0; c < kBlocks; ++c) {
-            if (PAGED)
-              tc::tma_load_4d(dst + c * (kBN * 128) + lane * rows * 128, map, full, 64 * c, hk,
-                              p.page > kBN ? k0 % p.page : 0, page_id);
-            else
-              tc::tma_load_4d(dst + c * (kBN * 128), map, full, 64 * c, hk, k0, b);
-          }
-        }
-        __syncwarp();
-      };
-      if (round > 0 && !wait_warp(&k_empty[st], (round - 1) & 1)) break;
-      copy(&k_full[st], &maps.k, sm + L::kOffK + st * L::kTile);
-      if (round > 0 && !wait_warp(&v_empty[st], (round - 1) & 1)) {
-        tc::mbar_wait(&k_full[st], round & 1);
-        break;
-      }
+      if (c >= NS && !wait_warp(&empty[st], (c / NS - 1) & 1)) break;
       if (PAGED) {
         // bit g: the 8 keys from 8 g on stand in an unusable page
-        const uint32_t bits = __ballot_sync(kFull, lane < kBN / 8 && ((bad >> (8 * lane / rows)) & 1));
+        const uint32_t bits = __ballot_sync(kFull, lane < kBN / 8 && ((bad[2] >> (8 * lane / rows)) & 1));
         if (lane == 0) bad_keys[st] = bits;
       }
-      copy(&v_full[st], &maps.v, sm + L::kOffV + st * L::kTile);
-      issued = i + 1;
+      if (lane == 0)
+        tc::mbar_arrive_expect_tx(&full[st], (uint32_t)(__popc(wanted[0]) + __popc(wanted[2])) * rows * 128 * kBlocks);
+      __syncwarp();
+      auto copy = [&](const CUtensorMap* map, unsigned char* dst, int step, uint32_t want, int id) {
+        if ((want >> lane) & 1) {
+          const int k0 = walk.tile(w0 + step) * kBN;
+#pragma unroll
+          for (int cb = 0; cb < kBlocks; ++cb) {
+            if (PAGED)
+              tc::tma_load_4d(dst + cb * (kBN * 128) + lane * rows * 128, map, &full[st], 64 * cb, hk,
+                              p.page > kBN ? k0 % p.page : 0, id);
+            else
+              tc::tma_load_4d(dst + cb * (kBN * 128), map, &full[st], 64 * cb, hk, k0, b);
+          }
+        }
+      };
+      copy(&maps.v, sm + L::kOffV + st * L::kTile, c - 2, wanted[2], page_id[2]);
+      copy(&maps.k, sm + L::kOffK + st * L::kTile, c, wanted[0], page_id[0]);
+      __syncwarp();
+      issued = c + 1;
     }
     // no copy may outlive the block, whatever became of its readers
-    for (int i = max(0, issued - NS); i < issued; ++i) {
-      tc::mbar_wait(&k_full[i % NS], (i / NS) & 1);
-      tc::mbar_wait(&v_full[i % NS], (i / NS) & 1);
-    }
+    for (int c = max(0, issued - NS); c < issued; ++c) tc::mbar_wait(&full[c % NS], (c / NS) & 1);
     for (int t = 0; t < ntiles; ++t) tc::mbar_wait(&q_full[t], 0);
   } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
     // =========================================================================== MMA issuers
@@ -199,59 +214,37 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     auto kstep = [](int R, int j) -> uint64_t { return (uint64_t)(((j >> 2) * (R * 128) + (j & 3) * 32) >> 4); };
     auto tile_at = [](int i) -> uint64_t { return (uint64_t)((i * L::kTile) >> 4); };
     const uint32_t cS = tb + t * 128, cO = tb + 256 + t * DP;
-    const Active act = active_tiles(pos0 + t * tok_tile, pos0 + t * tok_tile + (t ? ntok1 : ntok0) - 1, s.kv, p, t < ntiles);
+    const Steps act = steps_of(walk, w0, n, pos0 + t * tok_tile, pos0 + t * tok_tile + (t ? ntok1 : ntok0) - 1, s.kv, p,
+                               t < ntiles);
     if (tc::elect_one()) {
-      int si = 0, ns = 0, np = 0;  // next key tile to score; S and P V products issued
-      bool ok = t < ntiles && n > 0;
-      // S of the next key tile that these rows see, into buffer ns & 1. P of that buffer was multiplied by a
-      // product issued before (one thread's MMAs run in order). A tile that is not seen is let go of once its
-      // copy is there, so that both issuers' releases count for the same round of the stage.
-      auto scores = [&]() {
-        while (si < n) {
-          const int st = si % NS;
-          ok = wait_one(&k_full[st], (si / NS) & 1);
-          if (!ok) return;
-          const bool seen = act(walk.tile(w0 + si));
-          ++si;
-          if (!seen) {
-            mbar_arrive(&k_empty[st]);
-            continue;
-          }
+      int ns = 0, np = 0;  // S and P V products issued
+      bool ok = t < ntiles && n > 0 && wait_one(&q_full[t], 0);
+#pragma unroll 1
+      for (int c = 0; ok && c < n + 2; ++c) {
+        const int st = c % NS;
+        ok = wait_one(&full[st], (c / NS) & 1);
+        if (!ok) break;
+        if (c >= 2 && act(c - 2)) {
+          ok = wait_one(&p_full[t][np & 1], (np >> 1) & 1);
+          if (!ok) break;
+          tc::tmem_fence_after();
+          const uint64_t v = dV + tile_at(st);
+#pragma unroll
+          for (int j = 0; j < kBN / 16; ++j)
+            tc::mma_bf16_ts(cO, cS + (np & 1) * kBN + 8 * j, v + (uint64_t)(j * 2048 >> 4), kIdO, np > 0 || j > 0);
+          ++np;
+        }
+        if (c < n && act(c)) {
+          // into buffer ns & 1, over weights whose product was issued before: one thread's MMAs run in order
           const uint64_t k = dK + tile_at(st);
 #pragma unroll
           for (int j = 0; j < DP / 16; ++j)
             tc::mma_bf16_ss(cS + (ns & 1) * kBN, dQ + kstep(kBM, j), k + kstep(kBN, j), kIdS, j > 0);
           tc::mma_commit(&s_full[t][ns & 1]);
-          tc::mma_commit(&k_empty[st]);
           ++ns;
-          return;
         }
-      };
-      if (ok) ok = wait_one(&q_full[t], 0);
-      if (ok) scores();
-      if (ok) scores();
-#pragma unroll 1
-      for (int i = 0; ok && i < n; ++i) {
-        const int st = i % NS;
-        ok = wait_one(&v_full[st], (i / NS) & 1);
-        if (!ok) break;
-        if (!act(walk.tile(w0 + i))) {
-          mbar_arrive(&v_empty[st]);
-          continue;
-        }
-        ok = wait_one(&p_full[t][np & 1], (np >> 1) & 1);
-        if (!ok) break;
-        tc::tmem_fence_after();
-        const uint64_t v = dV + tile_at(st);
-#pragma unroll
-        for (int j = 0; j < kBN / 16; ++j)
-          tc::mma_bf16_ts(cO, cS + (np & 1) * kBN + 8 * j, v + (uint64_t)(j * 2048 >> 4), kIdO, np > 0 || j > 0);
-        tc::mma_commit(&o_done[t]);
-        tc::mma_commit(&v_empty[st]);
-        ++np;
-        scores();
+        tc::mma_commit(&empty[st]);  // (at once where nothing was issued)
       }
-      while (ok && si < n) scores();  // tiles behind the last one seen
       tc::mma_commit(&fin[t]);
     }
     __syncwarp();
@@ -261,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     const int t = warp >> 2;
     const int r = threadIdx.x & 127;
     const int ntok = t ? ntok1 : ntok0;
-    const Active act = active_tiles(pos0 + t * tok_tile, pos0 + t * tok_tile + ntok - 1, s.kv, p, ntok > 0);
+    const Steps act = steps_of(walk, w0, n, pos0 + t * tok_tile, pos0 + t * tok_tile + ntok - 1, s.kv, p, ntok > 0);
     const int tok = tok0 + t * tok_tile + r / G;
     const int pos = s.pos0 + tok;
     const int pmin = s.pos0 + tok0 + t * tok_tile, pmax = pmin + ntok - 1;
@@ -271,24 +264,23 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     float m = kNegInf, l = 0.f;
     int done = 0;
     bool ok = true;
-#pragma unroll 1
-    for (int i = 0; i < n; ++i) {
-      const int tile = walk.tile(w0 + i);
-      if (!act(tile)) continue;
-      const int k0 = tile * kBN;
-      ok = wait_warp(&s_full[t][done & 1], (done >> 1) & 1);
-      if (!ok) break;
+    // The warps of both tiles that share a scheduler form their weights in turn: see above.
+    const Steps other = steps_of(walk, w0, n, pos0 + (1 - t) * tok_tile, pos0 + (1 - t) * tok_tile + (t ? ntok0 : ntok1) - 1,
+                                 s.kv, p, t || ntiles > 1);
+    const int theirs = other.count(n);
+    const int my_turn = 1 + 2 * (warp & 3) + t, their_turn = 1 + 2 * (warp & 3) + 1 - t;
+    int last = 0;  // the step before this one
+    // Scores of step i into x (hidden ones -inf), and the row's reference moved where it has to. False: a wait expired.
+    auto look = [&](int i, int k0, bool there, uint32_t tP, float (&x)[kBN]) {
+      if (!there && !wait_warp(&s_full[t][done & 1], (done >> 1) & 1)) return false;
       tc::tmem_fence_after();
-      const uint32_t tSi = tS + (done & 1) * kBN;
-      float x[kBN];
-      tc::tmem_ld32(tSi, *reinterpret_cast<float(*)[32]>(&x[0]));
-      tc::tmem_ld32(tSi + 32, *reinterpret_cast<float(*)[32]>(&x[32]));
+      tc::tmem_ld32(tP, *reinterpret_cast<float(*)[32]>(&x[0]));
+      tc::tmem_ld32(tP + 32, *reinterpret_cast<float(*)[32]>(&x[32]));
       uint32_t bad = 0;
       if (PAGED) {
         // the list of unusable pages travels with the V tile
-        ok = wait_warp(&v_full[i % NS], (i / NS) & 1);
-        if (!ok) break;
-        bad = *(volatile uint32_t*)&bad_keys[i % NS];
+        if (!wait_warp(&full[(i + 2) % NS], ((i + 2) / NS) & 1)) return false;
+        bad = *(volatile uint32_t*)&bad_keys[(i + 2) % NS];
       }
       tc::tmem_wait_ld();
       const bool whole = k0 + kBN - 1 <= min(pmin, s.kv - 1) &&
@@ -312,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         if (PAGED && (k0 + kBN > s.kv || bad)) {
           // key r of the tile: its V row is cleared where there is no such key
           if (r < kBN && (k0 + r >= s.kv || ((bad >> (r / 8)) & 1))) {
-            unsigned char* v = sm + L::kOffV + (i % NS) * L::kTile + r * 128;
+            unsigned char* v = sm + L::kOffV + ((i + 2) % NS) * L::kTile + r * 128;
 #pragma unroll
             for (int c = 0; c < kBlocks; ++c)
 #pragma unroll
@@ -329,53 +321,76 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
 #pragma unroll
       for (int e = 0; e < 4; ++e) top4[e] = fmaxf(top4[e], x[kBN - 4 + e]);
       const float top = fmaxf(max3(top4[0], top4[1], top4[2]), top4[3]) * scale2;
-      if (done == 0) {
-        m = top;
-      } else {
-        const bool move = top > m + kSlack;
-        // (a row that has seen nothing yet has nothing to rescale)
-        if (__any_sync(kFull, move && m != kNegInf)) {
-          // O is this warp's once the last product into it is done (the one before was when this S came, and
-          // the next waits for this warp: the parity names one phase)
-          ok = wait_warp(&o_done[t], (done - 1) & 1);
-          if (!ok) break;
-          tc::tmem_fence_after();
-          const float f = move ? ex2(m - top) : 1.f;
-          l *= f;
+      const bool move = done == 0 || top > m + kSlack;
+      // (a row that has seen nothing yet has nothing to rescale)
+      if (__any_sync(kFull, move && m != kNegInf)) {
+        // O is this warp's once the last product into it is done, that is once its unit is let go of. (The
+        // unit that takes the stage next comes behind this tile's product, so the parity names one phase.)
+        if (!wait_warp(&empty[(last + 2) % NS], ((last + 2) / NS) & 1)) return false;
+        tc::tmem_fence_after();
+        const float f = move ? ex2(m - top) : 1.f;
+        l *= f;
 #pragma unroll 1
-          for (int c = 0; c < DP; c += 32) {
-            float o[32];
-            tc::tmem_ld32(tO + c, o);
-            tc::tmem_wait_ld();
+        for (int c = 0; c < DP; c += 16) {
+          float o[16];
+          tc::tmem_ld16(tO + c, o);
+          tc::tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] *= f;
-            tc::tmem_st32(tO + c, o);
+          for (int e = 0; e < 16; ++e) o[e] *= f;
+          tc::tmem_st16(tO + c, o);
+        }
+      }
+      if (move) m = top;
+      return true;
+    };
+    int i = 0;
+    while (i < n && !act(i)) ++i;
+    int k0 = walk.tile(w0 + i) * kBN;
+    bool there = false;  // S of step i is known to be ready
+#pragma unroll 1
+    while (i < n) {
+      const uint32_t tP = tS + (done & 1) * kBN;
+      float x[kBN];
+      ok = ok && look(i, k0, there, tP, x);
+      int next = i + 1;
+      while (next < n && !act(next)) ++next;
+      const int k0_next = walk.tile(w0 + next) * kBN;
+      // (a warp whose wait expired still takes and passes its turns: the other one is not left waiting)
+      if (t ? done < theirs : done > 0 && done <= theirs) turn_wait(my_turn);
+      // asked here, so that the answer comes while the exponentials run
+      const bool ready = tc::mbar_test(&s_full[t][(done + 1) & 1], ((done + 1) >> 1) & 1);
+      if (ok) {
+        const float ref = m == kNegInf ? 0.f : m;
+        const float2 s2 = make_float2(scale2, scale2), r2 = make_float2(-ref, -ref);
+        float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          float w[8];
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            float2 e = fma2(make_float2(x[16 * h + 2 * c], x[16 * h + 2 * c + 1]), s2, r2);
+            e.x = ex2(e.x);
+            e.y = ex2(e.y);
+            if (c & 1) sum1 = add2(sum1, e);
+            else sum0 = add2(sum0, e);
+            w[c] = __uint_as_float(pack_bf16(e.x, e.y));
           }
+          tc::tmem_st8(tP + 8 * h, w);
         }
-        if (move) m = top;
+        l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
       }
-      const float ref = m == kNegInf ? 0.f : m;
-      const float2 s2 = make_float2(scale2, scale2), r2 = make_float2(-ref, -ref);
-      float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float w[16];
-#pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          float2 e = fma2(make_float2(x[32 * h + 2 * c], x[32 * h + 2 * c + 1]), s2, r2);
-          e.x = ex2(e.x);
-          e.y = ex2(e.y);
-          if (c & 1) sum1 = add2(sum1, e);
-          else sum0 = add2(sum0, e);
-          w[c] = __uint_as_float(pack_bf16(e.x, e.y));
-        }
-        tc::tmem_st16(tSi + 16 * h, w);
+      if (t ? done + 1 < theirs : done < theirs) turn_pass(their_turn);
+      if (ok) {
+        tc::tmem_wait_st();
+        tc::tmem_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[t][done & 1]);
       }
-      l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
-      tc::tmem_wait_st();
-      tc::tmem_fence_before();
-      mbar_arrive(&p_full[t][done & 1]);
+      there = __all_sync(kFull, ready);
       ++done;
+      last = i;
+      i = next;
+      k0 = k0_next;
     }
     if (ok && done > 0) {
       ok = wait_warp(&fin[t], 0);

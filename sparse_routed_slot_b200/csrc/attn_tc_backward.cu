@@ -1,21 +1,21 @@
 // attn_tc_backward.cu -- gradients of window attention for bf16 inputs on the 5th-generation tensor cores.
 //
-// Two kernels, so that no sum depends on the order in which blocks finish (7 tile products per pair of
-// tiles against the 5 of one kernel that would add dq up with atomics):
-//   dk, dv: a block owns 128 keys and walks the packed query rows (token, head of the group) that see them
-//     S^T = K Q^T, dP^T = V dO^T            (fp32 in TMEM, a thread per key)
-//     P^T = 2^(S'^T - lse), dS^T = P^T (dP^T - delta)   -> bf16 in TMEM
-//     dV += P^T dO, dK += dS^T Q            (Q and dO as TMA wrote them, contracted over their rows)
-//   dq: a block owns 128 query rows and walks their keys
-//     S = Q K^T, dP = dO V^T, dS = P (dP - delta) -> bf16 in TMEM, dQ += dS K
-// P and dS are rounded to bf16 for their products (2^-9 each); delta comes from the stored o.
+// Two runs of one kernel, so that no sum depends on the order in which blocks finish (7 tile products per
+// pair of tiles against the 5 of one kernel that would add dq up with atomics). A block owns 128 rows
+// (A1, A2) and walks those they meet in tiles of 64 (B1, B2):
+//   dk, dv: A = keys (k, v), B = packed query rows (token, head of the group) that see them (q, dO)
+//   dq:     A = packed query rows (q, dO), B = the keys they see (k, v)
+//   S = A1 B1^T, E = A2 B2^T             fp32 in TMEM, a thread per row of A
+//   P = 2^(S' - lse), Z = P (E - delta)  -> bf16 over S and E (rounded here: the next products take bf16)
+//   G2 += Z B1  (dk or dq),  G1 += P B2  (dv; not in the dq run)
+// S and E have two buffers each and two groups of 128 threads take the steps in turn, so S and E of the
+// next step are there when a group comes back, and one group's exponentials run beside the other's loads.
+// The tiles of 64 leave room for four stages of B: with 128 and two, each step waited for its copies
+// (window train, dk and dv: 5500 cycles per 128 query rows; now 2900, of which the tensor core needs 2560:
+// S and E of 64 columns run at 3/4 rate, bound by their operands from shared memory).
 //
-// The order of the products keeps the tensor core busy through the exponentials. dk, dv (512 TMEM columns
-// in all: S^T, dP^T, dV, dK): dV_i, S_{i+1}, dK_i, dP_{i+1}: P_{i+1} is formed while dK_i and dP_{i+1} run,
-// dS_{i+1} while dV_{i+1} and S_{i+2} do. dq: dP_{i+1}, dQ_i, S_{i+2} with two S buffers: dS_i over S_i,
-// P_{i+1} formed during dP_{i+1}.
-//
-// Warps: 0-7 rows (warps 0-3 columns 0..63 of a tile, 4-7 columns 64..127), 8 copies, 9 MMA issuer.
+// Warps: 0-3 even steps, 4-7 odd steps, 8 copies (TMA), 9 MMA issuer.
+// TMEM columns: S buffers at 0 and 64, E buffers at 128 and 192, G2 at 256, G1 at 256 + DP.
 //
 // Keys below `sinks` are seen by every later row. Where that makes the first key tiles' walks much longer
 // than a window, the part behind the window is cut into chunks for further blocks; these leave fp32 sums of
@@ -30,64 +30,57 @@ namespace {
 
 using namespace attn;
 
-constexpr int kBM = 128, kBN = 128;
-constexpr int kThreads = 320, kRowThreads = 256;
+constexpr int kBM = 128, kBN = 64;
+constexpr int kThreads = 320;
 constexpr int kCopyWarp = 8, kMmaWarp = 9;
-constexpr int kChunkTiles = 16;  // query tiles per chunk behind the window
+constexpr int kStages = 4;
+constexpr int kMinChunk = 16;  // query tiles per chunk behind the window, at least
 constexpr int kMaxSinkTiles = 4;
 
+// A: the block's rows, B: the rows that pass by (of 1 = q or k, 2 = dO or v)
 struct Maps {
-  CUtensorMap q, k, v, dO;
+  CUtensorMap a1, a2, b1, b2;
 };
 
 template <int DP> struct Layout {
-  static constexpr int kTile = kBM * DP * 2;
-  static constexpr int kBytesKv = 6 * kTile + 1024;  // K, V, Q x 2, dO x 2
-  static constexpr int kBytesQ = 7 * kTile + 1024;   // Q, dO, K x 3, V x 2
+  static constexpr int kA = kBM * DP * 2, kB = kBN * DP * 2;
+  static constexpr int kOffB = 2 * kA;
+  static constexpr int kOffStat = kOffB + kStages * 2 * kB;
+  static constexpr int kBytes = kOffStat + kStages * 512 + 1024;
+  static_assert(kBytes <= 232448 - 1024, "shared memory budget");
 };
 
-// K step j (16 columns) of a K-major tile: 32 bytes inside a 64-column block, then the next block.
-RSM_DEV uint64_t kstep(int j) { return (uint64_t)(((j >> 2) * (kBM * 128) + (j & 3) * 32) >> 4); }
-// K step j (16 rows) of an MN-major tile.
-RSM_DEV uint64_t rstep(int j) { return (uint64_t)(j * 2048 >> 4); }
-// TMEM column of K step j of a bf16 operand written over an fp32 tile by two groups of warps: columns
-// 0..63 of the tile stand in its columns 0..31, columns 64..127 in its columns 64..95, so that no group
-// writes where the other still reads.
-RSM_DEV uint32_t acol(int j) { return (uint32_t)((j >> 2) * 64 + (j & 3) * 8); }
-
-template <int DP>
-RSM_DEV void product_ss(uint32_t d, uint64_t a, uint64_t b) {
-  constexpr uint32_t id = tc::idesc_bf16(kBM, kBN, 0, 0);
-#pragma unroll
-  for (int j = 0; j < DP / 16; ++j) tc::mma_bf16_ss(d, a + kstep(j), b + kstep(j), id, j > 0);
-}
-
-template <int DP>
-RSM_DEV void product_ts(uint32_t d, uint32_t a, uint64_t b, bool add) {
-  constexpr uint32_t id = tc::idesc_bf16(kBM, DP, 0, 1);
-#pragma unroll
-  for (int j = 0; j < kBN / 16; ++j) tc::mma_bf16_ts(d, a + acol(j), b + rstep(j), id, add || j > 0);
-}
-
-struct Setup {
-  unsigned char* sm;
-  uint32_t tb;
+// How the walks of the key tiles are cut.
+struct Chunks {
+  int tiles;       // key tiles
+  int sink_tiles;  // of them cut (0: none is)
+  int far;         // chunks behind the window, per cut tile
+  int size;        // query tiles per chunk
+  float* part;     // [pairs][sink_tiles][far + 1][128][2][D]
 };
 
-RSM_DEV unsigned char* aligned_smem(unsigned char* raw) {
-  return reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+// The packed rows' statistics, in tiles of 64 rows: -lse (base 2) of the rows, then -delta.
+RSM_DEV float* stat_of(float* stat, int64_t pair, int ntiles, int tok, int g, int tok_tile, int G) {
+  const int tile = tok / tok_tile;
+  return stat + (pair * ntiles + tile) * 2 * kBN + (tok - tile * tok_tile) * G + g;
 }
 
-// Rows [used, 128) of a tile, which no copy writes, as zeros (they are contracted over).
-template <int DP> RSM_DEV void clear_rows(unsigned char* tile, int used) {
-  for (int e = threadIdx.x; e < (kBM - used) * (DP / 8); e += kThreads) {
-    const int row = used + e / (DP / 8), c = e % (DP / 8);
-    *reinterpret_cast<uint4*>(tile + (c >> 3) * (kBM * 128) + row * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
-  }
+// Last query tile that a key tile's window reaches.
+RSM_DEV int window_last(int k1, int T, int window, int tok_tile) {
+  return (int)((min((int64_t)T, (int64_t)k1 + window) - 1) / tok_tile);
+}
+
+RSM_DEV float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+      "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
 }
 
 template <int NC> RSM_DEV void store_row(__nv_bfloat16* to, uint32_t tmem, float scale, int cols, bool live) {
-#pragma unroll
+#pragma unroll 1
   for (int c = 0; c < NC; c += 32) {
     float x[32];
     tc::tmem_ld32(tmem + c, x);
@@ -102,83 +95,86 @@ template <int NC> RSM_DEV void store_row(__nv_bfloat16* to, uint32_t tmem, float
   }
 }
 
-// How the walks of the key tiles are cut (host and device).
-struct Chunks {
-  int tiles;       // key tiles
-  int sink_tiles;  // of them cut (0: none is)
-  int far;         // chunks behind the window, per cut tile
-  float* part;     // [pairs][sink_tiles][far + 1][128][2][D]
-};
-
-// Last query tile that a key tile's window reaches.
-RSM_DEV int window_last(int k1, int T, int window, int tok_tile) {
-  return (int)((min((int64_t)T, (int64_t)k1 + window) - 1) / tok_tile);
-}
-
-template <int DP>
-__global__ void __launch_bounds__(kThreads, 1) attn_tc_dkv_kernel(const __grid_constant__ Maps maps, const AttnParams p,
-                                                                  int tok_tile, Chunks ch) {
+// ntiles: dq: query tiles of 128 rows per pair; otherwise query tiles of 64 rows (the statistics').
+template <int DP, bool DQ>
+__global__ void __launch_bounds__(kThreads, 1) attn_tc_backward_kernel(const __grid_constant__ Maps maps, const AttnParams p,
+                                                                       int ntiles, int stat_tiles, Chunks ch) {
   using L = Layout<DP>;
   constexpr int kBlocks = DP / 64;
   extern __shared__ unsigned char smem_raw[];
-  __shared__ uint64_t kv_full, q_full[2], q_empty[2], do_full[2], do_empty[2], st_full[2], s_full, dp_full, p_full,
-      ds_full, fin;
-  __shared__ __align__(16) float stat[2][2][kBM];  // per stage: lse (base 2) and delta of the rows
+  __shared__ uint64_t a_full, full[kStages], empty[kStages], s_full[2], w_full[2], fin;
   __shared__ uint32_t s_tbase;
 
-  // Blocks of the first key tiles, whose walks are longest, start first; behind them the far chunks.
-  const int pairs = p.Hkv * p.B;
-  const int pair = blockIdx.x % pairs, item = blockIdx.x / pairs;
-  const bool is_far = item >= ch.tiles;
-  const int kt = is_far ? (item - ch.tiles) % ch.sink_tiles : item;
-  const int chunk = is_far ? 1 + (item - ch.tiles) / ch.sink_tiles : 0;
-  const int hk = pair % p.Hkv, b = pair / p.Hkv;
   const int G = p.G, D = p.D, T = p.T;
-  const int k0 = kt * kBN;
-  const int k1 = min(k0 + kBN, T) - 1;
-  const bool cut = kt < ch.sink_tiles;
-  int j0 = k0 / tok_tile, j1;  // query tiles [j0, j1)
-  {
+  const int tok64 = kBN / G;              // tokens of a tile of 64 packed rows
+  const int tok_a = DQ ? kBM / G : 0;     // tokens of the block's query tile (dq)
+  const int rows_b = DQ ? kBN : tok64 * G;  // rows that a copy brings
+
+  // ---- what this block owns and walks
+  int pair, tile, chunk = 0;
+  bool is_far = false;
+  if (DQ) {
+    tile = ntiles - 1 - blockIdx.x % ntiles;  // the last tiles see the most keys: they start first
+    pair = blockIdx.x / ntiles;
+  } else {
+    // blocks of the first key tiles, whose walks are longest, start first; behind them the far chunks
+    const int pairs = p.Hkv * p.B;
+    const int item = blockIdx.x / pairs;
+    pair = blockIdx.x % pairs;
+    is_far = item >= ch.tiles;
+    tile = is_far ? (item - ch.tiles) % ch.sink_tiles : item;
+    chunk = is_far ? 1 + (item - ch.tiles) / ch.sink_tiles : 0;
+  }
+  const int hk = pair % p.Hkv, b = pair / p.Hkv;
+  const int tok0 = DQ ? tile * tok_a : 0;            // dq: the block's tokens [tok0, tok0 + ntok)
+  const int ntok = DQ ? min(tok_a, T - tok0) : 0;
+  const int key0 = DQ ? 0 : tile * kBM;              // dk, dv: the block's keys from key0 on
+  const bool cut = !DQ && tile < ch.sink_tiles;
+  Walk walk{0, 0, 0};
+  if (DQ) {
+    walk = key_walk(tok0, tok0 + ntok - 1, T, p.window, p.sinks, kBN);
+  } else {
+    const int k1 = min(key0 + kBM, T) - 1;
     int t0, t1;
-    query_range(k0, k1, T, p.window, p.sinks, t0, t1);
-    j1 = (t1 - 1) / tok_tile + 1;
+    query_range(key0, k1, T, p.window, p.sinks, t0, t1);
+    int j0 = t0 / tok64, j1 = (t1 - 1) / tok64 + 1;
     if (cut) {
-      const int w = window_last(k1, T, p.window, tok_tile) + 1;
+      const int w = window_last(k1, T, p.window, tok64) + 1;
       if (is_far) {
-        j0 = min(w + (chunk - 1) * kChunkTiles, j1);
-        j1 = min(j0 + kChunkTiles, j1);
+        j0 = min(w + (chunk - 1) * ch.size, j1);
+        j1 = min(j0 + ch.size, j1);
       } else {
         j1 = w;
       }
     }
+    walk.first = j0;
+    walk.n = j1 - j0;
   }
-  const int n = j1 - j0;
-  const int rows_tile = tok_tile * G;
+  const int n = walk.n;
 
-  unsigned char* sm = aligned_smem(smem_raw);
-  unsigned char *sK = sm, *sV = sm + L::kTile, *sQ = sm + 2 * L::kTile, *sO = sm + 4 * L::kTile;
+  unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (warp == kMmaWarp) tc::tmem_alloc(&s_tbase, 512);
   if (threadIdx.x == 0) {
-    tc::mbar_init(&kv_full, 1);
-    for (int i = 0; i < 2; ++i) {
-      tc::mbar_init(&q_full[i], 1);
-      tc::mbar_init(&q_empty[i], 1);
-      tc::mbar_init(&do_full[i], 1);
-      tc::mbar_init(&do_empty[i], 1);
-      tc::mbar_init(&st_full[i], 32);
+    tc::mbar_init(&a_full, 1);
+    for (int i = 0; i < kStages; ++i) {
+      tc::mbar_init(&full[i], 1);
+      tc::mbar_init(&empty[i], 1);
     }
-    tc::mbar_init(&s_full, 1);
-    tc::mbar_init(&dp_full, 1);
-    tc::mbar_init(&p_full, kRowThreads);
-    tc::mbar_init(&ds_full, kRowThreads);
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&s_full[i], 1);
+      tc::mbar_init(&w_full[i], 4);
+    }
     tc::mbar_init(&fin, 1);
     tc::fence_mbar_init();
   }
-  if (rows_tile < kBM) {
-    for (int i = 0; i < 2; ++i) {
-      clear_rows<DP>(sQ + i * L::kTile, rows_tile);
-      clear_rows<DP>(sO + i * L::kTile, rows_tile);
+  if constexpr (!DQ) {
+    // rows of a tile that no copy writes are contracted over all the same: zero
+    const int gap = kBN - rows_b;
+    for (int e = threadIdx.x; e < kStages * 2 * gap * (DP / 8); e += kThreads) {
+      const int c = e % (DP / 8), row = rows_b + e / (DP / 8) % gap, which = e / (DP / 8) / gap;
+      *reinterpret_cast<uint4*>(sm + L::kOffB + which * L::kB + (c >> 3) * (kBN * 128) + row * 128 + (c & 7) * 16) =
+          make_uint4(0, 0, 0, 0);
     }
     tc::fence_async_smem();
   }
@@ -186,192 +182,193 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_dkv_kernel(const __grid_c
   __syncthreads();
   tc::tmem_fence_after();
   const uint32_t tb = s_tbase;
-  const uint32_t cS = tb, cP = tb + 128, cV = tb + 256, cK = tb + 256 + DP;
+  const uint32_t c2 = tb + 256, c1 = tb + 256 + DP;
 
   if (warp == kCopyWarp) {
     // =========================================================================== copies
-    if (lane == 0) {
-      tc::mbar_arrive_expect_tx(&kv_full, 2 * L::kTile);
+    if (tc::elect_one()) {
+      const int head_a = DQ ? hk * G : hk, row_a = DQ ? tok0 : key0;
+      const int head_b = DQ ? hk : hk * G;
+      tc::mbar_arrive_expect_tx(&a_full, (uint32_t)(2 * (DQ ? tok_a * G : kBM) * 128 * kBlocks));
       for (int c = 0; c < kBlocks; ++c) {
-        tc::tma_load_4d(sK + c * (kBN * 128), &maps.k, &kv_full, 64 * c, hk, k0, b);
-        tc::tma_load_4d(sV + c * (kBN * 128), &maps.v, &kv_full, 64 * c, hk, k0, b);
+        tc::tma_load_4d(sm + c * (kBM * 128), &maps.a1, &a_full, 64 * c, head_a, row_a, b);
+        tc::tma_load_4d(sm + L::kA + c * (kBM * 128), &maps.a2, &a_full, 64 * c, head_a, row_a, b);
       }
+      int issued = 0;
+#pragma unroll 1
+      for (int i = 0; i < n; ++i) {
+        const int st = i % kStages;
+        if (i >= kStages && !wait_one(&empty[st], (i / kStages - 1) & 1)) break;
+        const int j = walk.tile(i);
+        const int row = DQ ? j * kBN : j * tok64;
+        unsigned char* dst = sm + L::kOffB + st * 2 * L::kB;
+        tc::mbar_arrive_expect_tx(&full[st], (uint32_t)(2 * rows_b * 128 * kBlocks + (DQ ? 0 : 512)));
+        if (!DQ)
+          tc::bulk_load(sm + L::kOffStat + st * 512, p.delta + ((int64_t)pair * stat_tiles + j) * 2 * kBN, 512, &full[st]);
+        for (int c = 0; c < kBlocks; ++c) {
+          tc::tma_load_4d(dst + c * (kBN * 128), &maps.b1, &full[st], 64 * c, head_b, row, b);
+          tc::tma_load_4d(dst + L::kB + c * (kBN * 128), &maps.b2, &full[st], 64 * c, head_b, row, b);
+        }
+        issued = i + 1;
+      }
+      // no copy may outlive the block, whatever became of its readers
+      tc::mbar_wait(&a_full, 0);
+      for (int i = max(0, issued - kStages); i < issued; ++i) tc::mbar_wait(&full[i % kStages], (i / kStages) & 1);
     }
     __syncwarp();
-    int nq = 0, ndo = 0;
-    for (int i = 0; i < n; ++i) {
-      const int st = i & 1, round = i >> 1;
-      const int tok = (j0 + i) * tok_tile;
-      auto copy = [&](uint64_t* full, const CUtensorMap* map, unsigned char* dst) {
-        if (lane == 0) {
-          tc::mbar_arrive_expect_tx(full, (uint32_t)(rows_tile * 128 * kBlocks));
-          for (int c = 0; c < kBlocks; ++c) tc::tma_load_4d(dst + c * (kBM * 128), map, full, 64 * c, hk * G, tok, b);
-        }
-        __syncwarp();
-      };
-      if (round > 0 && !wait_warp(&q_empty[st], (round - 1) & 1)) break;
-      copy(&q_full[st], &maps.q, sQ + st * L::kTile);
-      nq = i + 1;
-      // the stage's statistics were last read for a dS that the emptied Q tile's product used
-      const int rows = min(rows_tile, (T - tok) * G);
-      float a[4], d[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int r = lane + 32 * e;
-        const int64_t at = ((int64_t)b * T + tok + r / G) * p.H + hk * G + r % G;
-        a[e] = r < rows ? p.lse[at] * kLog2e : 0.f;
-        d[e] = r < rows ? p.delta[at] : 0.f;
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        stat[st][0][lane + 32 * e] = a[e];
-        stat[st][1][lane + 32 * e] = d[e];
-      }
-      mbar_arrive(&st_full[st]);
-      __syncwarp();
-      if (round > 0 && !wait_warp(&do_empty[st], (round - 1) & 1)) break;
-      copy(&do_full[st], &maps.dO, sO + st * L::kTile);
-      ndo = i + 1;
-    }
-    // no copy may outlive the block, whatever became of its readers
-    tc::mbar_wait(&kv_full, 0);
-    for (int i = max(0, nq - 2); i < nq; ++i) tc::mbar_wait(&q_full[i & 1], (i >> 1) & 1);
-    for (int i = max(0, ndo - 2); i < ndo; ++i) tc::mbar_wait(&do_full[i & 1], (i >> 1) & 1);
   } else if (warp == kMmaWarp) {
     // =========================================================================== MMA issuer
-    const uint64_t dK = tc::smem_desc(tc::smem_u32(sK), 16, 1024), dV = tc::smem_desc(tc::smem_u32(sV), 16, 1024);
-    const uint64_t dQ = tc::smem_desc(tc::smem_u32(sQ), 16, 1024), dO = tc::smem_desc(tc::smem_u32(sO), 16, 1024);
-    const uint64_t rQ = tc::smem_desc(tc::smem_u32(sQ), kBM * 128, 1024), rO = tc::smem_desc(tc::smem_u32(sO), kBM * 128, 1024);
-    auto stage = [](int i) -> uint64_t { return (uint64_t)(((i & 1) * L::kTile) >> 4); };
+    constexpr uint32_t kIdS = tc::idesc_bf16(kBM, kBN, 0, 0), kIdG = tc::idesc_bf16(kBM, DP, 0, 1);
+    const uint64_t dA = tc::smem_desc(tc::smem_u32(sm), 16, 1024);
+    const uint64_t dB = tc::smem_desc(tc::smem_u32(sm + L::kOffB), 16, 1024);
+    // the same tiles contracted over their rows: 64-column blocks 8 KB apart
+    const uint64_t rB = tc::smem_desc(tc::smem_u32(sm + L::kOffB), kBN * 128, 1024);
+    auto kstep = [](int R, int j) -> uint64_t { return (uint64_t)(((j >> 2) * (R * 128) + (j & 3) * 32) >> 4); };
     if (tc::elect_one()) {
-      auto scores = [&](int i) {
-        product_ss<DP>(cS, dK, dQ + stage(i));
-        tc::mma_commit(&s_full);
-      };
-      auto dprobs = [&](int i) {
-        product_ss<DP>(cP, dV, dO + stage(i));
-        tc::mma_commit(&dp_full);
-      };
-      bool ok = n > 0 && wait_one(&kv_full, 0) && wait_one(&q_full[0], 0);
-      if (ok) {
-        scores(0);
-        ok = wait_one(&do_full[0], 0);
-        if (ok) dprobs(0);
-      }
+      bool ok = wait_one(&a_full, 0);
 #pragma unroll 1
-      for (int i = 0; ok && i < n; ++i) {
-        const int nx = i + 1;
-        if (nx < n && !(ok = wait_one(&q_full[nx & 1], (nx >> 1) & 1))) break;
-        if (!(ok = wait_one(&p_full, i & 1))) break;
-        tc::tmem_fence_after();
-        product_ts<DP>(cV, cS, rO + stage(i), i > 0);
-        tc::mma_commit(&do_empty[i & 1]);
-        if (nx < n) {
-          scores(nx);
-          if (!(ok = wait_one(&do_full[nx & 1], (nx >> 1) & 1))) break;
+      for (int c = 0; ok && c < n + 2; ++c) {
+        if (c < n && !(ok = wait_one(&full[c % kStages], (c / kStages) & 1))) break;
+        if (c >= 2) {
+          const int i = c - 2, st = i % kStages;
+          if (!(ok = wait_one(&w_full[i & 1], (i >> 1) & 1))) break;
+          tc::tmem_fence_after();
+          const uint64_t r1 = rB + (uint64_t)((st * 2 * L::kB) >> 4), r2 = r1 + (uint64_t)(L::kB >> 4);
+          const uint32_t aP = tb + (i & 1) * kBN, aZ = tb + 128 + (i & 1) * kBN;
+          if (!DQ) {
+#pragma unroll
+            for (int j = 0; j < kBN / 16; ++j)
+              tc::mma_bf16_ts(c1, aP + 8 * j, r2 + (uint64_t)(j * 2048 >> 4), kIdG, i > 0 || j > 0);
+          }
+#pragma unroll
+          for (int j = 0; j < kBN / 16; ++j)
+            tc::mma_bf16_ts(c2, aZ + 8 * j, r1 + (uint64_t)(j * 2048 >> 4), kIdG, i > 0 || j > 0);
+          tc::mma_commit(&empty[st]);
         }
-        if (!(ok = wait_one(&ds_full, i & 1))) break;
-        tc::tmem_fence_after();
-        product_ts<DP>(cK, cP, rQ + stage(i), i > 0);
-        tc::mma_commit(&q_empty[i & 1]);
-        if (nx < n) dprobs(nx);
+        if (c < n) {
+          // into buffers c & 1, over weights whose products were issued before: one thread's MMAs run in order
+          const uint64_t b1 = dB + (uint64_t)((c % kStages * 2 * L::kB) >> 4), b2 = b1 + (uint64_t)(L::kB >> 4);
+          const uint64_t a2 = dA + (uint64_t)(L::kA >> 4);
+#pragma unroll
+          for (int j = 0; j < DP / 16; ++j)
+            tc::mma_bf16_ss(tb + (c & 1) * kBN, dA + kstep(kBM, j), b1 + kstep(kBN, j), kIdS, j > 0);
+#pragma unroll
+          for (int j = 0; j < DP / 16; ++j)
+            tc::mma_bf16_ss(tb + 128 + (c & 1) * kBN, a2 + kstep(kBM, j), b2 + kstep(kBN, j), kIdS, j > 0);
+          tc::mma_commit(&s_full[c & 1]);
+        }
       }
       tc::mma_commit(&fin);
     }
     __syncwarp();
     tc::mbar_wait(&fin, 0);  // every MMA issued is done before the block gives up its memory
   } else {
-    // =========================================================================== keys
-    const int half = warp >> 2;
+    // =========================================================================== rows of A
+    const int u = warp >> 2;
     const int r = threadIdx.x & 127;
-    const int key = k0 + r;
+    const int key = key0 + r;                                       // dk, dv
+    const int pos = tok0 + r / G;                                   // dq
+    const bool live = DQ ? r < ntok * G : key < T;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32);
-    const uint32_t tS = tc::tmem_addr(cS, lane_base, 64 * half), tP = tc::tmem_addr(cP, lane_base, 64 * half);
-    const float scale2 = p.scale * kLog2e;
+    const uint32_t tS = tc::tmem_addr(tb, lane_base, u * kBN), tE = tc::tmem_addr(tb, lane_base, 128 + u * kBN);
+    const float2 s2 = make_float2(p.scale * kLog2e, p.scale * kLog2e);
+    float2 nl = make_float2(0.f, 0.f), nd = nl;  // dq: the row's statistics
+    if (DQ && live) {
+      const float* st = stat_of(p.delta, pair, stat_tiles, pos, r % G, tok64, G);
+      nl = make_float2(st[0], st[0]);
+      nd = make_float2(st[kBN], st[kBN]);
+    }
     bool ok = true;
-    for (int i = 0; i < n; ++i) {
-      const int tok = (j0 + i) * tok_tile;
-      const int rows = min(rows_tile, (T - tok) * G);
-      // rows [lo, hi) of the tile see the key
-      const int lo = (key - tok) * G - 64 * half;
-      const int64_t end = key < p.sinks ? rows : min((int64_t)rows, ((int64_t)key + p.window - tok) * G);
-      const int hi = (int)max(end, (int64_t)0) - 64 * half;
-      const bool whole = __all_sync(kFull, lo <= 0 && hi >= 64);
-      const float4* sl = reinterpret_cast<const float4*>(&stat[i & 1][0][64 * half]);
-      const float4* sd = reinterpret_cast<const float4*>(&stat[i & 1][1][64 * half]);
-      if (!(ok = wait_warp(&st_full[i & 1], (i >> 1) & 1))) break;
-      if (!(ok = wait_warp(&s_full, i & 1))) break;
+#pragma unroll 1
+    for (int i = u; i < n; i += 2) {
+      // columns [lo, hi) of the step, and [0, sk), meet this row
+      const int j = walk.tile(i);
+      int lo, hi, sk = 0;
+      bool whole;
+      if (DQ) {
+        const int k0 = j * kBN;
+        hi = pos - k0 + 1;
+        lo = pos - p.window + 1 - k0;
+        sk = min(p.sinks - k0, hi);
+        whole = k0 + kBN - 1 <= tok0 && (tok0 + ntok - 1 - k0 < p.window || k0 + kBN - 1 < p.sinks);
+      } else {
+        const int tok = j * tok64;
+        const int rows = min(rows_b, (T - tok) * G);
+        lo = (key - tok) * G;
+        hi = key < p.sinks ? rows : (int)min((int64_t)rows, max((int64_t)0, ((int64_t)key + p.window - tok) * G));
+        whole = __all_sync(kFull, lo <= 0 && hi >= kBN);
+      }
+      const uint32_t m0 = whole ? ~0u : (below(hi) & ~below(lo)) | below(sk);
+      const uint32_t m1 = whole ? ~0u : (below(hi - 32) & ~below(lo - 32)) | below(sk - 32);
+      const float2* stl = reinterpret_cast<const float2*>(sm + L::kOffStat + (i % kStages) * 512);
+      if (!DQ && !(ok = wait_warp(&full[i % kStages], (i / kStages) & 1))) break;
+      if (!(ok = wait_warp(&s_full[u], (i >> 1) & 1))) break;
       tc::tmem_fence_after();
-      float x[64];
-      tc::tmem_ld32(tS, *reinterpret_cast<float(*)[32]>(&x[0]));
-      tc::tmem_ld32(tS + 32, *reinterpret_cast<float(*)[32]>(&x[32]));
-      tc::tmem_wait_ld();
-#pragma unroll
-      for (int c = 0; c < 64; c += 4) {
-        const float4 e = sl[c >> 2];
-        x[c] = ex2(fmaf(x[c], scale2, -e.x));
-        x[c + 1] = ex2(fmaf(x[c + 1], scale2, -e.y));
-        x[c + 2] = ex2(fmaf(x[c + 2], scale2, -e.z));
-        x[c + 3] = ex2(fmaf(x[c + 3], scale2, -e.w));
-      }
-      if (!whole) {
-#pragma unroll
-        for (int c = 0; c < 64; ++c)
-          if (c < lo || c >= hi) x[c] = 0.f;
-      }
-      {
-        float w[32];
-#pragma unroll
-        for (int c = 0; c < 32; ++c) w[c] = __uint_as_float(pack_bf16(x[2 * c], x[2 * c + 1]));
-        tc::tmem_st32(tS, w);
-      }
-      tc::tmem_wait_st();
-      tc::tmem_fence_before();
-      mbar_arrive(&p_full);
-      if (!(ok = wait_warp(&dp_full, i & 1))) break;
-      tc::tmem_fence_after();
-      float w[32];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        float y[32];
-        tc::tmem_ld32(tP + 32 * h, y);
+        float x[32], e[32];
+        tc::tmem_ld32(tS + 32 * h, x);
+        tc::tmem_ld32(tE + 32 * h, e);
         tc::tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < 32; c += 4) {
-          const float4 d = sd[(32 * h + c) >> 2];
-          const float* q = &x[32 * h + c];
-          // a row that does not see the key has a weight of zero and may have any dP: 0 * finite
-          w[16 * h + c / 2] = __uint_as_float(pack_bf16(q[0] * (y[c] - d.x), q[1] * (y[c + 1] - d.y)));
-          w[16 * h + c / 2 + 1] = __uint_as_float(pack_bf16(q[2] * (y[c + 2] - d.z), q[3] * (y[c + 3] - d.w)));
+        for (int c = 0; c < 32; c += 2) {
+          const float2 l2 = DQ ? nl : stl[16 * h + c / 2], d2 = DQ ? nd : stl[kBN / 2 + 16 * h + c / 2];
+          float2 w = fma2(make_float2(x[c], x[c + 1]), s2, l2);
+          w.x = ex2(w.x);
+          w.y = ex2(w.y);
+          const float2 z = mul2(w, add2(make_float2(e[c], e[c + 1]), d2));
+          x[c] = w.x; x[c + 1] = w.y;
+          e[c] = z.x; e[c + 1] = z.y;
         }
+        if (!whole) {
+          const uint32_t m = h ? m1 : m0;
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            if (!(m & (1u << c))) x[c] = e[c] = 0.f;
+        }
+        float w[16];
+        if (!DQ) {
+#pragma unroll
+          for (int c = 0; c < 16; ++c) w[c] = __uint_as_float(pack_bf16(x[2 * c], x[2 * c + 1]));
+          tc::tmem_st16(tS + 16 * h, w);
+        }
+#pragma unroll
+        for (int c = 0; c < 16; ++c) w[c] = __uint_as_float(pack_bf16(e[2 * c], e[2 * c + 1]));
+        tc::tmem_st16(tE + 16 * h, w);
       }
-      tc::tmem_st32(tP, w);
       tc::tmem_wait_st();
       tc::tmem_fence_before();
-      mbar_arrive(&ds_full);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&w_full[u]);
     }
     if (ok) ok = wait_warp(&fin, 0);
     if (ok) {
       tc::tmem_fence_after();
-      const uint32_t src = tc::tmem_addr(half ? cK : cV, lane_base, 0);
-      const float f = half ? p.scale : 1.f;
-      const bool to_part = cut && key < p.sinks;
-      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(half ? p.dk : p.dv);
-      const bool live = key < T && out && !is_far && !to_part && n > 0;
-      store_row<DP>(out + (((int64_t)b * T + key) * p.Hkv + hk) * D, src, f, D, live);
-      if (__any_sync(kFull, to_part && key < T)) {
-        float* to = ch.part + ((((int64_t)pair * ch.sink_tiles + kt) * (ch.far + 1) + chunk) * kBN + r) * 2 * D + half * D;
+      if (DQ) {
+        constexpr int kHalf = DP / 2;  // each group stores half of the columns
+        const int64_t row = ((int64_t)b * T + pos) * p.H + hk * G + r % G;
+        store_row<kHalf>(static_cast<__nv_bfloat16*>(p.dq) + row * D + u * kHalf, tc::tmem_addr(c2, lane_base, u * kHalf),
+                         p.scale, D - u * kHalf, live);
+      } else {
+        const uint32_t src = tc::tmem_addr(u ? c2 : c1, lane_base, 0);  // group 0 stores dv, group 1 dk
+        const float f = u ? p.scale : 1.f;
+        const bool to_part = cut && key < p.sinks;
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(u ? p.dk : p.dv);
+        store_row<DP>(out + (((int64_t)b * T + key) * p.Hkv + hk) * D, src, f, D, live && out && !is_far && !to_part);
+        if (__any_sync(kFull, to_part && live)) {
+          float* to = ch.part + ((((int64_t)pair * ch.sink_tiles + tile) * (ch.far + 1) + chunk) * kBM + r) * 2 * D + u * D;
+#pragma unroll 1
+          for (int c = 0; c < DP; c += 32) {
+            float x[32];
+            tc::tmem_ld32(src + c, x);
+            tc::tmem_wait_ld();
+            if (to_part && live) {
 #pragma unroll
-        for (int c = 0; c < DP; c += 32) {
-          float x[32];
-          tc::tmem_ld32(src + c, x);
-          tc::tmem_wait_ld();
-          if (to_part && key < T) {
-#pragma unroll
-            for (int e = 0; e < 32; e += 4)
-              if (c + e < D)
-                *reinterpret_cast<float4*>(to + c + e) =
-                    n > 0 ? make_float4(x[e] * f, x[e + 1] * f, x[e + 2] * f, x[e + 3] * f) : make_float4(0.f, 0.f, 0.f, 0.f);
+              for (int e = 0; e < 32; e += 4)
+                if (c + e < D)
+                  *reinterpret_cast<float4*>(to + c + e) = n > 0 ? make_float4(x[e] * f, x[e + 1] * f, x[e + 2] * f, x[e + 3] * f)
+                                                                 : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
           }
         }
       }
@@ -383,19 +380,47 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_dkv_kernel(const __grid_c
   if (warp == kMmaWarp) tc::tmem_dealloc(tb, 512);
 }
 
+// Statistics of every query row: -lse in base 2 and -delta, delta = dO . o; half a warp per row.
+__global__ void __launch_bounds__(256) stat_kernel(const AttnParams p, int64_t rows, int tok_tile, int ntiles) {
+  const int64_t row = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
+  if (row >= rows) return;
+  const int lane = threadIdx.x & 15;
+  const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(p.dO) + row * p.D;
+  const __nv_bfloat16* y = static_cast<const __nv_bfloat16*>(p.o) + row * p.D;
+  float sum = 0.f;
+  for (int d = lane * 8; d < p.D; d += 128) {
+    const uint4 a = *reinterpret_cast<const uint4*>(x + d), c = *reinterpret_cast<const uint4*>(y + d);
+    const uint32_t u[4] = {a.x, a.y, a.z, a.w}, v[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      sum = fmaf(__uint_as_float(u[i] << 16), __uint_as_float(v[i] << 16), sum);
+      sum = fmaf(__uint_as_float(u[i] & 0xffff0000u), __uint_as_float(v[i] & 0xffff0000u), sum);
+    }
+  }
+#pragma unroll
+  for (int d = 8; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffu << (threadIdx.x & 16), sum, d);
+  if (lane == 0) {
+    const int h = (int)(row % p.H);
+    const int64_t t = row / p.H;
+    float* to = stat_of(p.delta, t / p.T * p.Hkv + h / p.G, ntiles, (int)(t % p.T), h % p.G, tok_tile, p.G);
+    to[0] = -p.lse[row] * kLog2e;
+    to[kBN] = -sum;
+  }
+}
+
 // Adds the chunks of the sink rows up, in order, a warp per row.
 __global__ void __launch_bounds__(256) sink_sum_kernel(const AttnParams p, Chunks ch) {
   const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
-  const int r = (int)(w % kBN);
-  const int kt = (int)(w / kBN % ch.sink_tiles);
-  const int64_t pair = w / kBN / ch.sink_tiles;
-  const int key = kt * kBN + r;
+  const int r = (int)(w % kBM);
+  const int kt = (int)(w / kBM % ch.sink_tiles);
+  const int64_t pair = w / kBM / ch.sink_tiles;
+  const int key = kt * kBM + r;
   if (pair >= (int64_t)p.B * p.Hkv || key >= p.sinks || key >= p.T) return;
   const int hk = (int)(pair % p.Hkv);
   const int64_t b = pair / p.Hkv;
-  const float* part = ch.part + ((pair * ch.sink_tiles + kt) * (ch.far + 1) * kBN + r) * 2 * p.D;
-  const int64_t step = (int64_t)kBN * 2 * p.D;
+  const float* part = ch.part + ((pair * ch.sink_tiles + kt) * (ch.far + 1) * kBM + r) * 2 * p.D;
+  const int64_t step = (int64_t)kBM * 2 * p.D;
   const int64_t at = ((b * p.T + key) * p.Hkv + hk) * p.D;
   for (int d = lane * 2; d < 2 * p.D; d += 64) {
     float2 s = make_float2(0.f, 0.f);
@@ -409,248 +434,83 @@ __global__ void __launch_bounds__(256) sink_sum_kernel(const AttnParams p, Chunk
   }
 }
 
-template <int DP>
-__global__ void __launch_bounds__(kThreads, 1) attn_tc_dq_kernel(const __grid_constant__ Maps maps, const AttnParams p,
-                                                                 int tok_tile, int ntiles) {
-  using L = Layout<DP>;
-  constexpr int kBlocks = DP / 64;
-  extern __shared__ unsigned char smem_raw[];
-  __shared__ uint64_t q_full, k_full[3], k_empty[3], v_full[2], v_empty[2], s_full[2], dp_full, ds_full, fin;
-  __shared__ uint32_t s_tbase;
+size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-  const int tile = ntiles - 1 - blockIdx.x % ntiles;  // the last tiles see the most keys: they start first
-  const int pair = blockIdx.x / ntiles;
-  const int hk = pair % p.Hkv, b = pair / p.Hkv;
-  const int G = p.G, D = p.D, T = p.T;
-  const int tok0 = tile * tok_tile;
-  const int ntok = min(tok_tile, T - tok0);
-  const Walk walk = key_walk(tok0, tok0 + ntok - 1, T, p.window, p.sinks, kBN);
-  const int n = walk.n;  // at least 1: every row sees itself
-
-  unsigned char* sm = aligned_smem(smem_raw);
-  unsigned char *sQ = sm, *sO = sm + L::kTile, *sK = sm + 2 * L::kTile, *sV = sm + 5 * L::kTile;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (warp == kMmaWarp) tc::tmem_alloc(&s_tbase, 512);
-  if (threadIdx.x == 0) {
-    tc::mbar_init(&q_full, 1);
-    for (int i = 0; i < 3; ++i) {
-      tc::mbar_init(&k_full[i], 1);
-      tc::mbar_init(&k_empty[i], 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      tc::mbar_init(&v_full[i], 1);
-      tc::mbar_init(&v_empty[i], 1);
-      tc::mbar_init(&s_full[i], 1);
-    }
-    tc::mbar_init(&dp_full, 1);
-    tc::mbar_init(&ds_full, kRowThreads);
-    tc::mbar_init(&fin, 1);
-    tc::fence_mbar_init();
-  }
-  tc::tmem_fence_before();
-  __syncthreads();
-  tc::tmem_fence_after();
-  const uint32_t tb = s_tbase;
-  const uint32_t cS = tb, cP = tb + 256, cQ = tb + 384;  // S at 0 and 128
-
-  if (warp == kCopyWarp) {
-    // =========================================================================== copies
-    if (lane == 0) {
-      tc::mbar_arrive_expect_tx(&q_full, (uint32_t)(2 * tok_tile * G * 128 * kBlocks));
-      for (int c = 0; c < kBlocks; ++c) {
-        tc::tma_load_4d(sQ + c * (kBM * 128), &maps.q, &q_full, 64 * c, hk * G, tok0, b);
-        tc::tma_load_4d(sO + c * (kBM * 128), &maps.dO, &q_full, 64 * c, hk * G, tok0, b);
-      }
-    }
-    __syncwarp();
-    int nk = 0, nv = 0;
-    for (int i = 0; i < n; ++i) {
-      const int k0 = walk.tile(i) * kBN;
-      auto copy = [&](uint64_t* full, const CUtensorMap* map, unsigned char* dst) {
-        if (lane == 0) {
-          tc::mbar_arrive_expect_tx(full, L::kTile);
-          for (int c = 0; c < kBlocks; ++c) tc::tma_load_4d(dst + c * (kBN * 128), map, full, 64 * c, hk, k0, b);
-        }
-        __syncwarp();
-      };
-      if (i >= 3 && !wait_warp(&k_empty[i % 3], (i / 3 - 1) & 1)) break;
-      copy(&k_full[i % 3], &maps.k, sK + (i % 3) * L::kTile);
-      nk = i + 1;
-      if (i >= 2 && !wait_warp(&v_empty[i & 1], ((i >> 1) - 1) & 1)) break;
-      copy(&v_full[i & 1], &maps.v, sV + (i & 1) * L::kTile);
-      nv = i + 1;
-    }
-    // no copy may outlive the block, whatever became of its readers
-    tc::mbar_wait(&q_full, 0);
-    for (int i = max(0, nk - 3); i < nk; ++i) tc::mbar_wait(&k_full[i % 3], (i / 3) & 1);
-    for (int i = max(0, nv - 2); i < nv; ++i) tc::mbar_wait(&v_full[i & 1], (i >> 1) & 1);
-  } else if (warp == kMmaWarp) {
-    // =========================================================================== MMA issuer
-    const uint64_t dQ = tc::smem_desc(tc::smem_u32(sQ), 16, 1024), dO = tc::smem_desc(tc::smem_u32(sO), 16, 1024);
-    const uint64_t dK = tc::smem_desc(tc::smem_u32(sK), 16, 1024), dV = tc::smem_desc(tc::smem_u32(sV), 16, 1024);
-    const uint64_t rK = tc::smem_desc(tc::smem_u32(sK), kBN * 128, 1024);
-    auto at = [](int i) -> uint64_t { return (uint64_t)((i * L::kTile) >> 4); };
-    if (tc::elect_one()) {
-      bool ok = wait_one(&q_full, 0);
-      auto scores = [&](int i) {
-        ok = ok && wait_one(&k_full[i % 3], (i / 3) & 1);
-        if (!ok) return;
-        product_ss<DP>(cS + (i & 1) * 128, dQ, dK + at(i % 3));
-        tc::mma_commit(&s_full[i & 1]);
-      };
-      auto dprobs = [&](int i) {
-        product_ss<DP>(cP, dO, dV + at(i & 1));
-        tc::mma_commit(&dp_full);
-        tc::mma_commit(&v_empty[i & 1]);
-      };
-      scores(0);
-      ok = ok && wait_one(&v_full[0], 0);
-      if (ok) dprobs(0);
-      if (n > 1) scores(1);
-#pragma unroll 1
-      for (int i = 0; ok && i < n; ++i) {
-        if (i + 1 < n && !(ok = wait_one(&v_full[(i + 1) & 1], ((i + 1) >> 1) & 1))) break;
-        if (!(ok = wait_one(&ds_full, i & 1))) break;
-        tc::tmem_fence_after();
-        if (i + 1 < n) dprobs(i + 1);
-        product_ts<DP>(cQ, cS + (i & 1) * 128, rK + at(i % 3), i > 0);
-        tc::mma_commit(&k_empty[i % 3]);
-        if (i + 2 < n) scores(i + 2);
-      }
-      tc::mma_commit(&fin);
-    }
-    __syncwarp();
-    tc::mbar_wait(&fin, 0);  // every MMA issued is done before the block gives up its memory
-  } else {
-    // =========================================================================== rows
-    const int half = warp >> 2;
-    const int r = threadIdx.x & 127;
-    const int pos = tok0 + r / G;
-    const bool live = r < ntok * G;
-    const int64_t row = ((int64_t)b * T + pos) * p.H + hk * G + r % G;
-    const float lse = live ? p.lse[row] * kLog2e : 0.f, delta = live ? p.delta[row] : 0.f;
-    const uint32_t lane_base = (uint32_t)((warp & 3) * 32);
-    const uint32_t tS = tc::tmem_addr(cS, lane_base, 64 * half), tP = tc::tmem_addr(cP, lane_base, 64 * half);
-    const float scale2 = p.scale * kLog2e;
-    bool ok = true;
-    for (int i = 0; i < n; ++i) {
-      const int k0 = walk.tile(i) * kBN + 64 * half;
-      if (!(ok = wait_warp(&s_full[i & 1], (i >> 1) & 1))) break;
-      tc::tmem_fence_after();
-      const uint32_t tSi = tS + (i & 1) * 128;
-      float x[64];
-      tc::tmem_ld32(tSi, *reinterpret_cast<float(*)[32]>(&x[0]));
-      tc::tmem_ld32(tSi + 32, *reinterpret_cast<float(*)[32]>(&x[32]));
-      tc::tmem_wait_ld();
-#pragma unroll
-      for (int c = 0; c < 64; ++c) x[c] = ex2(fmaf(x[c], scale2, -lse));
-      const bool whole = k0 + 63 <= tok0 && (tok0 + ntok - 1 - k0 < p.window || k0 + 63 < p.sinks);
-      if (!whole) {
-        const int hi = pos - k0, lo = pos - p.window + 1 - k0, sk = p.sinks - k0;
-#pragma unroll
-        for (int c = 0; c < 64; ++c)
-          if (c > hi || (c < lo && c >= sk)) x[c] = 0.f;
-      }
-      if (!(ok = wait_warp(&dp_full, i & 1))) break;
-      tc::tmem_fence_after();
-      float w[32];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float y[32];
-        tc::tmem_ld32(tP + 32 * h, y);
-        tc::tmem_wait_ld();
-#pragma unroll
-        for (int c = 0; c < 32; c += 2)
-          w[16 * h + c / 2] = __uint_as_float(
-              pack_bf16(x[32 * h + c] * (y[c] - delta), x[32 * h + c + 1] * (y[c + 1] - delta)));
-      }
-      tc::tmem_st32(tSi, w);
-      tc::tmem_wait_st();
-      tc::tmem_fence_before();
-      mbar_arrive(&ds_full);
-    }
-    if (ok) ok = wait_warp(&fin, 0);
-    if (ok) {
-      tc::tmem_fence_after();
-      constexpr int kHalf = DP / 2;
-      store_row<kHalf>(static_cast<__nv_bfloat16*>(p.dq) + row * D + half * kHalf, tc::tmem_addr(cQ, lane_base, half * kHalf),
-                       p.scale, D - half * kHalf, live);
-    }
-  }
-  tc::tmem_fence_before();
-  __syncthreads();
-  tc::tmem_fence_after();
-  if (warp == kMmaWarp) tc::tmem_dealloc(tb, 512);
+int stat_tiles(const AttnParams& p) {
+  const int tok = kBN / p.G;
+  return (p.T + tok - 1) / tok;
 }
 
-size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
+size_t stat_bytes(const AttnParams& p) {
+  return up256((size_t)p.B * p.Hkv * stat_tiles(p) * 2 * kBN * sizeof(float));
+}
 
 Chunks chunks_for(const AttnParams& p) {
   Chunks ch{};
-  const int tok = kBM / p.G;
-  ch.tiles = (p.T + kBN - 1) / kBN;
-  const int ns = std::min((std::min(p.sinks, p.T) + kBN - 1) / kBN, ch.tiles);
-  const int nq = (p.T + tok - 1) / tok;
-  const int near = (int)((std::min<int64_t>(p.T, (int64_t)kBN - 1 + p.window) - 1) / tok) + 1;
-  // worth it where the part behind the window is longer than two chunks: a cut costs each chunk's block
-  // its own K and V tile and the sum of the parts
-  if (ns > 0 && ns <= kMaxSinkTiles && nq - near > 2 * kChunkTiles) {
+  const int tok = kBN / p.G;
+  ch.tiles = (p.T + kBM - 1) / kBM;
+  const int ns = std::min((std::min(p.sinks, p.T) + kBM - 1) / kBM, ch.tiles);
+  const int nq = stat_tiles(p);
+  const int near = (int)((std::min<int64_t>(p.T, (int64_t)kBM - 1 + p.window) - 1) / tok) + 1;
+  // Worth it where the part behind the window is longer than the part inside: a cut costs each chunk's block
+  // its own K and V tile and the sum of the parts, and the longest walk is what the kernel ends with
+  // (1537 tokens, window 200, groups of 3: 110 us uncut, 33 us cut).
+  const int size = std::max(kMinChunk, near);
+  if (ns > 0 && ns <= kMaxSinkTiles && nq - near > near) {
     ch.sink_tiles = ns;
-    ch.far = (nq - near + kChunkTiles - 1) / kChunkTiles;
+    ch.size = size;
+    ch.far = (nq - near + size - 1) / size;
   }
   return ch;
 }
 
 size_t part_bytes(const AttnParams& p, const Chunks& ch) {
-  return up256((size_t)p.B * p.Hkv * ch.sink_tiles * (ch.sink_tiles ? ch.far + 1 : 0) * kBN * 2 * p.D * sizeof(float));
+  return up256((size_t)p.B * p.Hkv * ch.sink_tiles * (ch.sink_tiles ? ch.far + 1 : 0) * kBM * 2 * p.D * sizeof(float));
 }
 
-template <int DP> cudaError_t launch_dp(const Maps& maps, const AttnParams& p, const Chunks& ch, cudaStream_t stream) {
-  const int tok = kBM / p.G;
+template <int DP, bool DQ>
+cudaError_t launch_run(const Maps& maps, const AttnParams& p, const Chunks& ch, cudaStream_t stream) {
+  cudaError_t e = set_smem_limit<attn_tc_backward_kernel<DP, DQ>>(Layout<DP>::kBytes);
+  if (e != cudaSuccess) return e;
   const int64_t pairs = (int64_t)p.B * p.Hkv;
-  if (p.dk || p.dv) {
-    cudaError_t e = set_smem_limit<attn_tc_dkv_kernel<DP>>(Layout<DP>::kBytesKv);
-    if (e != cudaSuccess) return e;
-    const int64_t grid = pairs * (ch.tiles + (int64_t)ch.sink_tiles * ch.far);
-    if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    attn_tc_dkv_kernel<DP><<<(unsigned)grid, kThreads, Layout<DP>::kBytesKv, stream>>>(maps, p, tok, ch);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    if (ch.sink_tiles) {
-      sink_sum_kernel<<<(unsigned)((pairs * ch.sink_tiles * kBN + 7) / 8), 256, 0, stream>>>(p, ch);
-      e = cudaGetLastError();
-      if (e != cudaSuccess) return e;
-    }
-  }
-  if (p.dq) {
-    cudaError_t e = set_smem_limit<attn_tc_dq_kernel<DP>>(Layout<DP>::kBytesQ);
-    if (e != cudaSuccess) return e;
-    const int64_t ntiles = (p.T + tok - 1) / tok;
-    if (ntiles * pairs > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    attn_tc_dq_kernel<DP><<<(unsigned)(ntiles * pairs), kThreads, Layout<DP>::kBytesQ, stream>>>(maps, p, tok, (int)ntiles);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-  }
-  return cudaSuccess;
+  const int tok = kBM / p.G;
+  const int ntiles = (p.T + tok - 1) / tok;
+  const int64_t grid = DQ ? pairs * ntiles : pairs * (ch.tiles + (int64_t)ch.sink_tiles * ch.far);
+  if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  attn_tc_backward_kernel<DP, DQ><<<(unsigned)grid, kThreads, Layout<DP>::kBytes, stream>>>(maps, p, ntiles, stat_tiles(p), ch);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || DQ || !ch.sink_tiles) return e;
+  sink_sum_kernel<<<(unsigned)((pairs * ch.sink_tiles * kBM + 7) / 8), 256, 0, stream>>>(p, ch);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
-size_t attn_tc_backward_bytes(const AttnParams& p) { return part_bytes(p, chunks_for(p)); }
+size_t attn_tc_backward_bytes(const AttnParams& p) { return stat_bytes(p) + part_bytes(p, chunks_for(p)); }
 
-cudaError_t launch_attn_tc_backward(const AttnParams& p, float* part, cudaStream_t stream) {
-  Maps maps;
+cudaError_t launch_attn_tc_backward(const AttnParams& params, void* workspace, cudaStream_t stream) {
+  AttnParams p = params;
+  p.delta = static_cast<float*>(workspace);
+  Chunks ch = chunks_for(p);
+  ch.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + stat_bytes(p));
+  const int64_t rows = (int64_t)p.B * p.T * p.H;
+  stat_kernel<<<(unsigned)((rows + 15) / 16), 256, 0, stream>>>(p, rows, kBN / p.G, stat_tiles(p));
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
   const uint64_t D = p.D, H = p.H, Hkv = p.Hkv, T = p.T, B = p.B;
-  const uint32_t tok = (uint32_t)(kBM / p.G);
   const std::array<uint64_t, 4> qd{D, H, T, B}, kd{D, Hkv, T, B};
   const std::array<uint64_t, 3> qs{D, H * D, T * H * D}, ks{D, Hkv * D, T * Hkv * D};
-  const std::array<uint32_t, 4> qb{64, (uint32_t)p.G, tok, 1}, kb{64, 1, (uint32_t)kBN, 1};
-  if (!make_map_bf16(&maps.q, p.q, qd, qs, qb) || !make_map_bf16(&maps.dO, p.dO, qd, qs, qb) ||
-      !make_map_bf16(&maps.k, p.k, kd, ks, kb) || !make_map_bf16(&maps.v, p.v, kd, ks, kb))
+  auto q_map = [&](CUtensorMap* m, const void* x, int rows) {
+    return make_map_bf16(m, x, qd, qs, {64, (uint32_t)p.G, (uint32_t)(rows / p.G), 1});
+  };
+  auto k_map = [&](CUtensorMap* m, const void* x, int rows) { return make_map_bf16(m, x, kd, ks, {64, 1, (uint32_t)rows, 1}); };
+  Maps kv, dq;
+  if (!k_map(&kv.a1, p.k, kBM) || !k_map(&kv.a2, p.v, kBM) || !q_map(&kv.b1, p.q, kBN) || !q_map(&kv.b2, p.dO, kBN) ||
+      !q_map(&dq.a1, p.q, kBM) || !q_map(&dq.a2, p.dO, kBM) || !k_map(&dq.b1, p.k, kBN) || !k_map(&dq.b2, p.v, kBN))
     return cudaErrorInvalidValue;
-  Chunks ch = chunks_for(p);
-  ch.part = part;
-  return p.D <= 64 ? launch_dp<64>(maps, p, ch, stream) : launch_dp<128>(maps, p, ch, stream);
+  if (p.dk || p.dv) e = p.D <= 64 ? launch_run<64, false>(kv, p, ch, stream) : launch_run<128, false>(kv, p, ch, stream);
+  if (e == cudaSuccess && p.dq) e = p.D <= 64 ? launch_run<64, true>(dq, p, ch, stream) : launch_run<128, true>(dq, p, ch, stream);
+  return e;
 }
 
 }  // namespace rsm

@@ -119,7 +119,7 @@ size_t delta_bytes(const rsm_window_backward_args& a) { return up256((size_t)a.B
 
 size_t window_backward_bytes(const rsm_window_backward_args& a) {
   const rsm::AttnParams p = window_params(a);
-  return delta_bytes(a) + (rsm::attn_tc_supported(p, a.dtype) ? rsm::attn_tc_backward_bytes(p) : 0);
+  return rsm::attn_tc_supported(p, a.dtype) ? rsm::attn_tc_backward_bytes(p) : delta_bytes(a);
 }
 
 rsm_status check_cache(int B, int N, int Hkv, int D, int num_pages, int page_size, int table_width) {
@@ -246,12 +246,13 @@ rsm_status rsm_window_backward(const rsm_window_backward_args* a, void* stream) 
   p.lse = const_cast<float*>(a->lse);
   p.dO = a->dO;
   p.dq = a->dq; p.dk = a->dk; p.dv = a->dv;
-  p.delta = static_cast<float*>(a->workspace);
-  if (e == cudaSuccess) e = rsm::launch_attn_delta(p, a->dtype, st);
-  if (e == cudaSuccess)
-    e = rsm::attn_tc_supported(p, a->dtype)
-            ? rsm::launch_attn_tc_backward(p, reinterpret_cast<float*>(static_cast<char*>(a->workspace) + delta_bytes(*a)), st)
-            : rsm::launch_attn_simt_backward(p, a->dtype, st);
+  if (e == cudaSuccess && rsm::attn_tc_supported(p, a->dtype)) {
+    e = rsm::launch_attn_tc_backward(p, a->workspace, st);
+  } else if (e == cudaSuccess) {
+    p.delta = static_cast<float*>(a->workspace);
+    e = rsm::launch_attn_delta(p, a->dtype, st);
+    if (e == cudaSuccess) e = rsm::launch_attn_simt_backward(p, a->dtype, st);
+  }
   return finish(e, "rsm_window_backward");
 }
 

@@ -78,10 +78,10 @@ cudaError_t launch_attn_simt_backward(const AttnParams& p, rsm_dtype dtype, cuda
 bool attn_tc_supported(const AttnParams& p, rsm_dtype dtype);
 int attn_tc_splits(const AttnParams& p);
 cudaError_t launch_attn_tc(const AttnParams& p, cudaStream_t stream);
-// Its gradients (attn_tc_backward.cu), dense only; `part` holds attn_tc_backward_bytes(p) bytes.
+// Its gradients (attn_tc_backward.cu), dense only; the workspace holds attn_tc_backward_bytes(p) bytes.
 size_t attn_tc_backward_bytes(const AttnParams& p);
-cudaError_t launch_attn_tc_backward(const AttnParams& p, float* part, cudaStream_t stream);
-// delta = dO . o for every row (the first step of every backward).
+cudaError_t launch_attn_tc_backward(const AttnParams& p, void* workspace, cudaStream_t stream);
+// delta = dO . o for every row (the first step of the fp32 backward).
 cudaError_t launch_attn_delta(const AttnParams& p, rsm_dtype dtype, cudaStream_t stream);
 // Joins the partial results of p.splits blocks into o and lse.
 cudaError_t launch_attn_combine(const AttnParams& p, rsm_dtype dtype, cudaStream_t stream);

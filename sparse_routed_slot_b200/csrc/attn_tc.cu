@@ -45,7 +45,7 @@ constexpr int kCopyWarp = 8, kMmaWarp = 9;  // and kMmaWarp + 1
 constexpr float kSlack = 32.f;  // how far (log2) the running maximum may pass the reference
 
 struct Maps {
-  CUtensorMap q, k, v;
+  CUtensorMap q, k, v, o;
 };
 
 template <int DP> struct Layout {
@@ -396,11 +396,26 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       ok = wait_warp(&fin[t], 0);
       tc::tmem_fence_after();
     }
-    if (ok && ntok > 0) {
-      const bool live = r < ntok * G;
-      const int64_t at = (s.row0 + tok) * p.H + hk * G + r % G;
-      const int64_t total = (int64_t)p.T * (PAGED ? 1 : p.B) * p.H;
-      const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;  // (a NaN stays one)
+    const bool live = r < ntok * G;
+    const int64_t at = (s.row0 + tok) * p.H + hk * G + r % G;
+    const int64_t total = (int64_t)p.T * (PAGED ? 1 : p.B) * p.H;
+    const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;  // (a NaN stays one)
+    // Whole tiles go through the query tile's memory, which is done with, to a tensor store; so does the last
+    // tile of a dense sequence, whose rows behind the end the store leaves out. Behind the end of a paged one
+    // stand the next sequence's rows.
+    if (p.splits == 1 && done > 0 && (!PAGED || ntok == tok_tile)) {
+      unsigned char* to = sm + t * L::kQ;
+      if (ok) stage_row<DP>(to, r, 0, tO, inv);
+      tc::fence_async_smem();
+      group_sync(9 + t, 128);
+      if (ok && r == 0) {
+        const int64_t first = (PAGED ? s.row0 : 0) + tok0 + t * tok_tile;
+        for (int c = 0; c < kBlocks; ++c)
+          tc::tma_store_4d(&maps.o, to + c * (kBM * 128), 64 * c, hk * G, (int)first, PAGED ? 0 : b);
+        tc::bulk_commit_group();
+        tc::bulk_wait_read_all();
+      }
+    } else if (ok && ntok > 0) {
 #pragma unroll 1
       for (int c = 0; c < DP; c += 32) {
         float o[32];
@@ -427,11 +442,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
           }
         }
       }
-      if (live) {
-        const float lse = l == 0.f ? kNegInf : (m + log2f(l)) * kLn2;
-        if (p.splits > 1) p.part_lse[split * total + at] = lse;
-        else if (p.lse) p.lse[at] = lse;
-      }
+    }
+    if (ok && live) {
+      const float lse = l == 0.f ? kNegInf : (m + log2f(l)) * kLn2;
+      if (p.splits > 1) p.part_lse[split * total + at] = lse;
+      else if (p.lse) p.lse[at] = lse;
     }
   }
   tc::tmem_fence_before();
@@ -484,7 +499,9 @@ cudaError_t launch_attn_tc(const AttnParams& p, cudaStream_t stream) {
   const bool paged = p.table != nullptr;
   const uint64_t T = p.T, B = paged ? 1 : p.B;
   const int tok = token_tile(p);
-  bool ok = make_map_bf16(&maps.q, p.q, {D, H, T, B}, {D, H * D, T * H * D}, {64, (uint32_t)p.G, (uint32_t)tok, 1});
+  bool ok = true;
+  for (auto [m, base] : {std::pair<CUtensorMap*, const void*>{&maps.q, p.q}, {&maps.o, p.o}})
+    ok = ok && make_map_bf16(m, base, {D, H, T, B}, {D, H * D, T * H * D}, {64, (uint32_t)p.G, (uint32_t)tok, 1});
   if (paged) {
     const uint64_t page = p.page, pages = p.num_pages;
     const uint32_t rows = (uint32_t)std::min(p.page, kBN);

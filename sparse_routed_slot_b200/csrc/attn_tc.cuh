@@ -63,5 +63,40 @@ RSM_DEV uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&t);
 }
 
+// NC fp32 columns of a thread's row in TMEM, times `scale`, as bf16 into row r of a tile that a tensor store
+// takes (64-column blocks of 128 swizzled rows), from column `c0` of the tile on.
+template <int NC> RSM_DEV void stage_row(unsigned char* tile, int r, int c0, uint32_t tmem, float scale) {
+#pragma unroll 1
+  for (int c = 0; c < NC; c += 32) {
+    float x[32];
+    tc::tmem_ld32(tmem + c, x);
+    tc::tmem_wait_ld();
+#pragma unroll
+    for (int e = 0; e < 32; e += 8) {
+      const int k = (c0 + c + e) >> 3;
+      *reinterpret_cast<uint4*>(tile + (k >> 3) * (128 * 128) + r * 128 + (((k & 7) ^ (r & 7)) << 4)) =
+          make_uint4(pack_bf16(x[e] * scale, x[e + 1] * scale), pack_bf16(x[e + 2] * scale, x[e + 3] * scale),
+                     pack_bf16(x[e + 4] * scale, x[e + 5] * scale), pack_bf16(x[e + 6] * scale, x[e + 7] * scale));
+    }
+  }
+}
+// The same columns straight to memory, 16 bytes at a time.
+template <int NC> RSM_DEV void store_row(__nv_bfloat16* to, uint32_t tmem, float scale, int cols, bool live) {
+#pragma unroll 1
+  for (int c = 0; c < NC; c += 32) {
+    float x[32];
+    tc::tmem_ld32(tmem + c, x);
+    tc::tmem_wait_ld();
+    if (!live) continue;
+#pragma unroll
+    for (int e = 0; e < 32; e += 8)
+      if (c + e < cols)
+        *reinterpret_cast<uint4*>(to + c + e) =
+            make_uint4(pack_bf16(x[e] * scale, x[e + 1] * scale), pack_bf16(x[e + 2] * scale, x[e + 3] * scale),
+                       pack_bf16(x[e + 4] * scale, x[e + 5] * scale), pack_bf16(x[e + 6] * scale, x[e + 7] * scale));
+  }
+}
+RSM_DEV void group_sync(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
+
 }  // namespace attn
 }  // namespace rsm

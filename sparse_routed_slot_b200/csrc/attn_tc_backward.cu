@@ -11,10 +11,13 @@
 // S and E have two buffers each and two groups of 128 threads take the steps in turn, so S and E of the
 // next step are there when a group comes back, and one group's exponentials run beside the other's loads.
 // The tiles of 64 leave room for four stages of B: with 128 and two, each step waited for its copies
-// (window train, dk and dv: 5500 cycles per 128 query rows; now 2900, of which the tensor core needs 2560:
-// S and E of 64 columns run at 3/4 rate, bound by their operands from shared memory).
+// (5500 cycles per 128 query rows for dk and dv, of which the tensor core needs 2560: S and E of 64 columns
+// run at 3/4 rate, bound by their operands from shared memory).
 //
-// Warps: 0-3 even steps, 4-7 odd steps, 8 copies (TMA), 9 MMA issuer.
+// S, E and G are issued by threads of two warps: a satisfied wait costs an issuer 200 cycles in which it
+// queues nothing, and one that had both (two waits per step) left the tensor core idle 2 of 5 cycles.
+//
+// Warps: 0-3 even steps, 4-7 odd steps, 8 copies (TMA), 9 issuer of S and E, 10 issuer of G1 and G2.
 // TMEM columns: S buffers at 0 and 64, E buffers at 128 and 192, G2 at 256, G1 at 256 + DP.
 //
 // Keys below `sinks` are seen by every later row. Where that makes the first key tiles' walks much longer
@@ -31,15 +34,15 @@ namespace {
 using namespace attn;
 
 constexpr int kBM = 128, kBN = 64;
-constexpr int kThreads = 320;
-constexpr int kCopyWarp = 8, kMmaWarp = 9;
+constexpr int kThreads = 352;
+constexpr int kCopyWarp = 8, kScoreWarp = 9, kGradWarp = 10;
 constexpr int kStages = 4;
 constexpr int kMinChunk = 16;  // query tiles per chunk behind the window, at least
 constexpr int kMaxSinkTiles = 4;
 
-// A: the block's rows, B: the rows that pass by (of 1 = q or k, 2 = dO or v)
+// A: the block's rows, B: the rows that pass by (of 1 = q or k, 2 = dO or v); g1, g2: the results
 struct Maps {
-  CUtensorMap a1, a2, b1, b2;
+  CUtensorMap a1, a2, b1, b2, g1, g2;
 };
 
 template <int DP> struct Layout {
@@ -77,22 +80,6 @@ RSM_DEV float2 mul2(float2 a, float2 b) {
       : "=f"(d.x), "=f"(d.y)
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return d;
-}
-
-template <int NC> RSM_DEV void store_row(__nv_bfloat16* to, uint32_t tmem, float scale, int cols, bool live) {
-#pragma unroll 1
-  for (int c = 0; c < NC; c += 32) {
-    float x[32];
-    tc::tmem_ld32(tmem + c, x);
-    tc::tmem_wait_ld();
-    if (!live) continue;
-#pragma unroll
-    for (int e = 0; e < 32; e += 8)
-      if (c + e < cols)
-        *reinterpret_cast<uint4*>(to + c + e) =
-            make_uint4(pack_bf16(x[e] * scale, x[e + 1] * scale), pack_bf16(x[e + 2] * scale, x[e + 3] * scale),
-                       pack_bf16(x[e + 4] * scale, x[e + 5] * scale), pack_bf16(x[e + 6] * scale, x[e + 7] * scale));
-  }
 }
 
 // ntiles: dq: query tiles of 128 rows per pair; otherwise query tiles of 64 rows (the statistics').
@@ -154,7 +141,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_backward_kernel(const __g
 
   unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (warp == kMmaWarp) tc::tmem_alloc(&s_tbase, 512);
+  if (warp == kScoreWarp) tc::tmem_alloc(&s_tbase, 512);
   if (threadIdx.x == 0) {
     tc::mbar_init(&a_full, 1);
     for (int i = 0; i < kStages; ++i) {
@@ -165,7 +152,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_backward_kernel(const __g
       tc::mbar_init(&s_full[i], 1);
       tc::mbar_init(&w_full[i], 4);
     }
-    tc::mbar_init(&fin, 1);
+    tc::mbar_init(&fin, 2);
     tc::fence_mbar_init();
   }
   if constexpr (!DQ) {
@@ -216,52 +203,63 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_backward_kernel(const __g
       for (int i = max(0, issued - kStages); i < issued; ++i) tc::mbar_wait(&full[i % kStages], (i / kStages) & 1);
     }
     __syncwarp();
-  } else if (warp == kMmaWarp) {
-    // =========================================================================== MMA issuer
-    constexpr uint32_t kIdS = tc::idesc_bf16(kBM, kBN, 0, 0), kIdG = tc::idesc_bf16(kBM, DP, 0, 1);
-    const uint64_t dA = tc::smem_desc(tc::smem_u32(sm), 16, 1024);
+  } else if (warp == kScoreWarp) {
+    // =========================================================================== issuer of S and E
+    constexpr uint32_t kId = tc::idesc_bf16(kBM, kBN, 0, 0);
+    const uint64_t a1 = tc::smem_desc(tc::smem_u32(sm), 16, 1024), a2 = a1 + (uint64_t)(L::kA >> 4);
     const uint64_t dB = tc::smem_desc(tc::smem_u32(sm + L::kOffB), 16, 1024);
-    // the same tiles contracted over their rows: 64-column blocks 8 KB apart
-    const uint64_t rB = tc::smem_desc(tc::smem_u32(sm + L::kOffB), kBN * 128, 1024);
     auto kstep = [](int R, int j) -> uint64_t { return (uint64_t)(((j >> 2) * (R * 128) + (j & 3) * 32) >> 4); };
     if (tc::elect_one()) {
       bool ok = wait_one(&a_full, 0);
 #pragma unroll 1
-      for (int c = 0; ok && c < n + 2; ++c) {
-        if (c < n && !(ok = wait_one(&full[c % kStages], (c / kStages) & 1))) break;
-        if (c >= 2) {
-          const int i = c - 2, st = i % kStages;
-          if (!(ok = wait_one(&w_full[i & 1], (i >> 1) & 1))) break;
-          tc::tmem_fence_after();
-          const uint64_t r1 = rB + (uint64_t)((st * 2 * L::kB) >> 4), r2 = r1 + (uint64_t)(L::kB >> 4);
-          const uint32_t aP = tb + (i & 1) * kBN, aZ = tb + 128 + (i & 1) * kBN;
-          if (!DQ) {
+      for (int c = 0; ok && c < n; ++c) {
+        // buffer c & 1 is free once the products of step c - 2 are done, which lets go of its stage, too
+        ok = wait_one(&full[c % kStages], (c / kStages) & 1) &&
+             (c < 2 || wait_one(&empty[(c - 2) % kStages], ((c - 2) / kStages) & 1));
+        if (!ok) break;
+        tc::tmem_fence_after();
+        const uint64_t b1 = dB + (uint64_t)((c % kStages * 2 * L::kB) >> 4), b2 = b1 + (uint64_t)(L::kB >> 4);
 #pragma unroll
-            for (int j = 0; j < kBN / 16; ++j)
-              tc::mma_bf16_ts(c1, aP + 8 * j, r2 + (uint64_t)(j * 2048 >> 4), kIdG, i > 0 || j > 0);
-          }
+        for (int j = 0; j < DP / 16; ++j)
+          tc::mma_bf16_ss(tb + (c & 1) * kBN, a1 + kstep(kBM, j), b1 + kstep(kBN, j), kId, j > 0);
 #pragma unroll
-          for (int j = 0; j < kBN / 16; ++j)
-            tc::mma_bf16_ts(c2, aZ + 8 * j, r1 + (uint64_t)(j * 2048 >> 4), kIdG, i > 0 || j > 0);
-          tc::mma_commit(&empty[st]);
-        }
-        if (c < n) {
-          // into buffers c & 1, over weights whose products were issued before: one thread's MMAs run in order
-          const uint64_t b1 = dB + (uint64_t)((c % kStages * 2 * L::kB) >> 4), b2 = b1 + (uint64_t)(L::kB >> 4);
-          const uint64_t a2 = dA + (uint64_t)(L::kA >> 4);
-#pragma unroll
-          for (int j = 0; j < DP / 16; ++j)
-            tc::mma_bf16_ss(tb + (c & 1) * kBN, dA + kstep(kBM, j), b1 + kstep(kBN, j), kIdS, j > 0);
-#pragma unroll
-          for (int j = 0; j < DP / 16; ++j)
-            tc::mma_bf16_ss(tb + 128 + (c & 1) * kBN, a2 + kstep(kBM, j), b2 + kstep(kBN, j), kIdS, j > 0);
-          tc::mma_commit(&s_full[c & 1]);
-        }
+        for (int j = 0; j < DP / 16; ++j)
+          tc::mma_bf16_ss(tb + 128 + (c & 1) * kBN, a2 + kstep(kBM, j), b2 + kstep(kBN, j), kId, j > 0);
+        tc::mma_commit(&s_full[c & 1]);
       }
       tc::mma_commit(&fin);
     }
     __syncwarp();
     tc::mbar_wait(&fin, 0);  // every MMA issued is done before the block gives up its memory
+  } else if (warp == kGradWarp) {
+    // =========================================================================== issuer of G1 and G2
+    constexpr uint32_t kId = tc::idesc_bf16(kBM, DP, 0, 1);
+    // the tiles of B contracted over their rows: 64-column blocks 8 KB apart, 16 rows 2 KB
+    const uint64_t rB = tc::smem_desc(tc::smem_u32(sm + L::kOffB), kBN * 128, 1024);
+    if (tc::elect_one()) {
+      bool ok = true;
+#pragma unroll 1
+      for (int i = 0; ok && i < n; ++i) {
+        const int st = i % kStages;
+        ok = wait_one(&full[st], (i / kStages) & 1) && wait_one(&w_full[i & 1], (i >> 1) & 1);
+        if (!ok) break;
+        tc::tmem_fence_after();
+        const uint64_t r1 = rB + (uint64_t)((st * 2 * L::kB) >> 4), r2 = r1 + (uint64_t)(L::kB >> 4);
+        const uint32_t aP = tb + (i & 1) * kBN, aZ = tb + 128 + (i & 1) * kBN;
+        if (!DQ) {
+#pragma unroll
+          for (int j = 0; j < kBN / 16; ++j)
+            tc::mma_bf16_ts(c1, aP + 8 * j, r2 + (uint64_t)(j * 2048 >> 4), kId, i > 0 || j > 0);
+        }
+#pragma unroll
+        for (int j = 0; j < kBN / 16; ++j)
+          tc::mma_bf16_ts(c2, aZ + 8 * j, r1 + (uint64_t)(j * 2048 >> 4), kId, i > 0 || j > 0);
+        tc::mma_commit(&empty[st]);
+      }
+      tc::mma_commit(&fin);
+    }
+    __syncwarp();
+    tc::mbar_wait(&fin, 0);
   } else {
     // =========================================================================== rows of A
     const int u = warp >> 2;
@@ -342,18 +340,38 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_backward_kernel(const __g
       if (lane == 0) mbar_arrive(&w_full[u]);
     }
     if (ok) ok = wait_warp(&fin, 0);
-    if (ok) {
-      tc::tmem_fence_after();
-      if (DQ) {
-        constexpr int kHalf = DP / 2;  // each group stores half of the columns
-        const int64_t row = ((int64_t)b * T + pos) * p.H + hk * G + r % G;
-        store_row<kHalf>(static_cast<__nv_bfloat16*>(p.dq) + row * D + u * kHalf, tc::tmem_addr(c2, lane_base, u * kHalf),
-                         p.scale, D - u * kHalf, live);
-      } else {
-        const uint32_t src = tc::tmem_addr(u ? c2 : c1, lane_base, 0);  // group 0 stores dv, group 1 dk
-        const float f = u ? p.scale : 1.f;
-        const bool to_part = cut && key < p.sinks;
-        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(u ? p.dk : p.dv);
+    tc::tmem_fence_after();
+    // The tiles of A are done with: the results go through their memory to tensor stores, which leave out
+    // what lies behind the last row and column. (Stored by the row's threads, 16 bytes each at the rows'
+    // distance, they took 6000 cycles.)
+    if (DQ) {
+      constexpr int kHalf = DP / 2;  // each group has half of the columns
+      if (ok) stage_row<kHalf>(sm, r, u * kHalf, tc::tmem_addr(c2, lane_base, u * kHalf), p.scale);
+      tc::fence_async_smem();
+      group_sync(1, 256);
+      if (ok && threadIdx.x == 0) {
+        for (int c = 0; c < kBlocks; ++c) tc::tma_store_4d(&maps.g2, sm + c * (kBM * 128), 64 * c, hk * G, tok0, b);
+        tc::bulk_commit_group();
+        tc::bulk_wait_read_all();
+      }
+    } else {
+      const uint32_t src = tc::tmem_addr(u ? c2 : c1, lane_base, 0);  // group 0 has dv, group 1 dk
+      const float f = u ? p.scale : 1.f;
+      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(u ? p.dk : p.dv);
+      if (!cut) {
+        unsigned char* to = sm + u * L::kA;
+        if (ok) stage_row<DP>(to, r, 0, src, f);
+        tc::fence_async_smem();
+        group_sync(1 + u, 128);
+        if (ok && out && r == 0) {
+          for (int c = 0; c < kBlocks; ++c)
+            tc::tma_store_4d(u ? &maps.g2 : &maps.g1, to + c * (kBM * 128), 64 * c, hk, key0, b);
+          tc::bulk_commit_group();
+          tc::bulk_wait_read_all();
+        }
+      } else if (ok) {
+        // the sink rows' sums go to the workspace; the first block of a cut tile has all of its other rows
+        const bool to_part = key < p.sinks;
         store_row<DP>(out + (((int64_t)b * T + key) * p.Hkv + hk) * D, src, f, D, live && out && !is_far && !to_part);
         if (__any_sync(kFull, to_part && live)) {
           float* to = ch.part + ((((int64_t)pair * ch.sink_tiles + tile) * (ch.far + 1) + chunk) * kBM + r) * 2 * D + u * D;
@@ -377,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_backward_kernel(const __g
   tc::tmem_fence_before();
   __syncthreads();
   tc::tmem_fence_after();
-  if (warp == kMmaWarp) tc::tmem_dealloc(tb, 512);
+  if (warp == kScoreWarp) tc::tmem_dealloc(tb, 512);
 }
 
 // Statistics of every query row: -lse in base 2 and -delta, delta = dO . o; half a warp per row.
@@ -508,6 +526,11 @@ cudaError_t launch_attn_tc_backward(const AttnParams& params, void* workspace, c
   if (!k_map(&kv.a1, p.k, kBM) || !k_map(&kv.a2, p.v, kBM) || !q_map(&kv.b1, p.q, kBN) || !q_map(&kv.b2, p.dO, kBN) ||
       !q_map(&dq.a1, p.q, kBM) || !q_map(&dq.a2, p.dO, kBM) || !k_map(&dq.b1, p.k, kBN) || !k_map(&dq.b2, p.v, kBN))
     return cudaErrorInvalidValue;
+  // (a result that is not wanted has a map that nothing is stored through)
+  if (!k_map(&kv.g1, p.dv ? p.dv : p.v, kBM) || !k_map(&kv.g2, p.dk ? p.dk : p.k, kBM) ||
+      !q_map(&dq.g2, p.dq ? p.dq : p.q, kBM))
+    return cudaErrorInvalidValue;
+  dq.g1 = dq.g2;
   if (p.dk || p.dv) e = p.D <= 64 ? launch_run<64, false>(kv, p, ch, stream) : launch_run<128, false>(kv, p, ch, stream);
   if (e == cudaSuccess && p.dq) e = p.D <= 64 ? launch_run<64, true>(dq, p, ch, stream) : launch_run<128, true>(dq, p, ch, stream);
   return e;

@@ -13,85 +13,98 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _lib
-from .api import _DTYPES, _need, _stream
+from .api import _DTYPES
 
 _NO_SIZE = ctypes.c_size_t(-1).value
 _ACTS = {"silu": _lib.RSM_ACT_SILU, "sigmoid": _lib.RSM_ACT_SIGMOID}
+_INT_MAX = 2**31 - 1
+_ref = ctypes.byref
+
+# A single-token step is a few microseconds on the device, so the checks below are written to cost little
+# where they find nothing: one test per tensor, and the words only for one that fails.
 
 
-def _ptr(t):
-    return None if t is None else t.data_ptr()
+def _fault(t, name, dtype, shape, index):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        return f"{name} must be a CUDA tensor"
+    if not t.is_contiguous():
+        return f"{name} must be contiguous"
+    if t.dtype != dtype:
+        return f"{name} must be {dtype}, got {t.dtype}"
+    if tuple(t.shape) != tuple(shape):
+        return f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}"
+    return f"{name} must be on cuda:{index}, got {t.device}"
 
 
-def _same_device(dev, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} must be on {dev}, got {t.device}")
+def _ptr(t, name, dtype, shape, index):
+    """The address of a contiguous tensor of that type, shape and device; None for None."""
+    if t is None:
+        return None
+    if not (isinstance(t, torch.Tensor) and t.get_device() == index and t.dtype is dtype and t.shape == shape and
+            t.is_contiguous()):
+        raise ValueError(_fault(t, name, dtype, shape, index))
+    return t.data_ptr()
 
 
-def _dtype(t: torch.Tensor, name: str) -> int:
+def _given(t, name, dtype, shape, index):
+    """_ptr of a tensor that has to be there."""
+    if t is None:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return _ptr(t, name, dtype, shape, index)
+
+
+def _first(t, name, dims):
+    """(type, shape, device index) of the tensor that the others have to agree with."""
     if not isinstance(t, torch.Tensor) or t.dtype not in _DTYPES:
         raise ValueError(f"{name} must be a float32 or bfloat16 tensor")
-    return _DTYPES[t.dtype]
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if dims and t.dim() != len(dims):
+        raise ValueError(f"{name} must be [{','.join(dims)}], got {tuple(t.shape)}")
+    return t.dtype, t.shape, t.get_device()
 
 
-def _call(fn, args, dev):
-    """Runs a library call on the device's current stream, with that device current."""
-    if dev.index == torch.cuda.current_device():
-        _lib.check(fn(ctypes.byref(args), _stream(dev)))
-    else:
-        with torch.cuda.device(dev):
-            _lib.check(fn(ctypes.byref(args), _stream(dev)))
-
-
-def _workspace(size_fn, fn, args, dev, workspace):
-    """Fills args.workspace: the caller's (a uint8 tensor) where it is large enough, else a new one.
-    Returns the tensor, which has to live until the call is queued."""
-    if dev.index == torch.cuda.current_device():
-        need = size_fn(ctypes.byref(args))
-    else:
-        with torch.cuda.device(dev):
-            need = size_fn(ctypes.byref(args))
-    if need == _NO_SIZE:
-        _lib.check(fn(ctypes.byref(args), None))  # raises with the reason
-    if need:
-        if workspace is None or workspace.numel() < need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        else:
-            _need(workspace, "workspace", torch.uint8)
-            _same_device(dev, workspace=workspace)
-        args.workspace, args.workspace_bytes = workspace.data_ptr(), workspace.numel()
-    return workspace
-
-
-def _fill(a, **kw):
-    for n, v in kw.items():
-        setattr(a, n, v)
-    return a
+def _run(fn, args, index, size_fn=None, workspace=None):
+    """A library call on the device's current stream, with that device current. With size_fn it gets a
+    workspace: the caller's (a uint8 tensor) where that is large enough, else a new one of torch's."""
+    if index != torch._C._cuda_getDevice():
+        with torch.cuda.device(index):
+            return _run(fn, args, index, size_fn, workspace)
+    if size_fn is not None:
+        need = size_fn(_ref(args))
+        if need == _NO_SIZE:
+            _lib.check(fn(_ref(args), None))  # raises with the reason
+        if need:
+            if workspace is None or workspace.numel() < need:
+                workspace = torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", index))
+            args.workspace = _given(workspace, "workspace", torch.uint8, workspace.shape, index)
+            args.workspace_bytes = workspace.numel()
+    status = fn(_ref(args), torch._C._cuda_getCurrentRawStream(index))
+    if status:
+        _lib.check(status)
 
 
 def _scale(scale, D):
-    return 1.0 / math.sqrt(D) if scale is None else float(scale)
+    return 1.0 / math.sqrt(D) if scale is None and D else float(scale or 0.0)
+
+
+def _int(x):
+    """A C int; past its range the largest one, which is as good as no limit."""
+    return min(int(x), _INT_MAX)
 
 
 # ------------------------------------------------------------------------------ window attention
-def _window_args(a, q, k, v, window, sinks, scale, validate):
-    dt = _dtype(q, "q")
-    _need(q, "q")
-    if q.dim() != 4:
-        raise ValueError(f"q must be [B,T,H,D], got {tuple(q.shape)}")
-    B, T, H, D = q.shape
-    _need(k, "k", q.dtype)
-    if k.dim() != 4:
-        raise ValueError(f"k must be [B,T,Hkv,D], got {tuple(k.shape)}")
-    Hkv = k.shape[2]
-    _need(k, "k", shape=(B, T, Hkv, D))
-    _need(v, "v", q.dtype, (B, T, Hkv, D))
-    _same_device(q.device, k=k, v=v)
-    # a window longer than the sequence is the whole sequence; the C int holds no more than 2^31 - 1
-    return _fill(a, B=B, T=T, H=H, Hkv=Hkv, D=D, window=min(int(window), 2**31 - 1), sinks=min(int(sinks), 2**31 - 1),
-                 dtype=dt, scale=_scale(scale, D), q=q.data_ptr(), k=k.data_ptr(), v=v.data_ptr(),
-                 flags=_lib.RSM_FLAG_VALIDATE if validate else 0)
+def _window_args(cls, q, k, v, window, sinks, scale, validate):
+    dtype, shape, index = _first(q, "q", "BTHD")
+    B, T, H, D = shape
+    _, kshape, _ = _first(k, "k", ("B", "T", "Hkv", "D"))
+    Hkv = kshape[2]
+    kshape = torch.Size((B, T, Hkv, D))
+    a = cls(B, T, H, Hkv, D, _int(window), _int(sinks), _DTYPES[dtype], _scale(scale, D), _ptr(q, "q", dtype, shape, index),
+            _ptr(k, "k", dtype, kshape, index), _given(v, "v", dtype, kshape, index))
+    if validate:
+        a.flags = _lib.RSM_FLAG_VALIDATE
+    return a, dtype, shape, kshape, index
 
 
 def window_forward(q, k, v, window: int, sinks: int = 0, scale=None, *, lse: bool = False, validate: bool = False,
@@ -101,20 +114,16 @@ def window_forward(q, k, v, window: int, sinks: int = 0, scale=None, *, lse: boo
 
     Returns dict(o [B,T,H,D] in q's dtype, lse [B,T,H] fp32 or None). `out` may supply preallocated
     tensors under the same keys."""
-    a = _window_args(_lib.WindowArgs(), q, k, v, window, sinks, scale, validate)
-    out = out or {}
-    o, ls = out.get("o"), out.get("lse")
+    a, dtype, shape, _, index = _window_args(_lib.WindowArgs, q, k, v, window, sinks, scale, validate)
+    o = ls = None
+    if out:
+        o, ls = out.get("o"), out.get("lse")
     if o is None:
         o = torch.empty_like(q)
-    else:
-        _need(o, "o", q.dtype, q.shape)
-    if ls is not None:
-        _need(ls, "lse", torch.float32, q.shape[:3])
-    elif lse:
-        ls = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
-    _same_device(q.device, o=o, lse=ls)
-    a.o, a.lse = o.data_ptr(), _ptr(ls)
-    _call(_lib.load().rsm_window_forward, a, q.device)
+    if ls is None and lse:
+        ls = torch.empty(shape[:3], dtype=torch.float32, device=q.device)
+    a.o, a.lse = _ptr(o, "o", dtype, shape, index), _ptr(ls, "lse", torch.float32, shape[:3], index)
+    _run(_lib.load().rsm_window_forward, a, index)
     return {"o": o, "lse": ls}
 
 
@@ -122,26 +131,21 @@ def window_backward(q, k, v, o, lse, dO, window: int, sinks: int = 0, scale=None
                     validate: bool = False, out=None, workspace=None):
     """Gradients of window_forward: its inputs, its o and lse, and dO [B,T,H,D] in q's dtype.
     Returns dict(dq, dk, dv) in q's dtype (None where `need` says so)."""
-    a = _window_args(_lib.WindowBackwardArgs(), q, k, v, window, sinks, scale, validate)
-    _need(o, "o", q.dtype, q.shape)
-    _need(lse, "lse", torch.float32, q.shape[:3])
-    _need(dO, "dO", q.dtype, q.shape)
-    out = dict(out or {})
-    for name, like, wanted in zip(("dq", "dk", "dv"), (q, k, v), need):
-        if not wanted:
-            out[name] = None
-            continue
-        if out.get(name) is None:
-            out[name] = torch.empty_like(like)
-        _need(out[name], name, like.dtype, like.shape)
-        setattr(a, name, out[name].data_ptr())
-    _same_device(q.device, o=o, lse=lse, dO=dO, **out)
-    a.o, a.lse, a.dO = o.data_ptr(), lse.data_ptr(), dO.data_ptr()
+    a, dtype, shape, kshape, index = _window_args(_lib.WindowBackwardArgs, q, k, v, window, sinks, scale, validate)
+    a.o, a.dO = _given(o, "o", dtype, shape, index), _given(dO, "dO", dtype, shape, index)
+    a.lse = _given(lse, "lse", torch.float32, shape[:3], index)
+    got = {}
+    for name, like, size, wanted in zip(("dq", "dk", "dv"), (q, k, v), (shape, kshape, kshape), need):
+        g = None
+        if wanted:
+            g = out.get(name) if out else None
+            if g is None:
+                g = torch.empty_like(like)
+            setattr(a, name, _ptr(g, name, dtype, size, index))
+        got[name] = g
     L = _lib.load()
-    ws = _workspace(L.rsm_window_backward_workspace_size, L.rsm_window_backward, a, q.device, workspace)
-    _call(L.rsm_window_backward, a, q.device)
-    del ws
-    return out
+    _run(L.rsm_window_backward, a, index, L.rsm_window_backward_workspace_size, workspace)
+    return got
 
 
 class WindowFunction(torch.autograd.Function):
@@ -167,36 +171,35 @@ class WindowFunction(torch.autograd.Function):
 
 
 # ------------------------------------------------------------------------------- paged attention
-def _cache_args(a, new, k_cache, v_cache, page_table, cu_q, kv_len):
-    _need(k_cache, "k_cache", new.dtype)
-    if k_cache.dim() != 4:
-        raise ValueError(f"k_cache must be [pages, page_size, Hkv, D], got {tuple(k_cache.shape)}")
-    pages, page, Hkv, D = k_cache.shape
-    _need(v_cache, "v_cache", new.dtype, k_cache.shape)
-    _need(page_table, "page_table", torch.int32)
-    if page_table.dim() != 2:
-        raise ValueError(f"page_table must be [B, width], got {tuple(page_table.shape)}")
-    B = page_table.shape[0]
-    _need(cu_q, "cu_q", torch.int32, (B + 1,))
-    _need(kv_len, "kv_len", torch.int32, (B,))
-    _same_device(new.device, k_cache=k_cache, v_cache=v_cache, page_table=page_table, cu_q=cu_q, kv_len=kv_len)
-    return _fill(a, B=B, N=new.shape[0], Hkv=Hkv, D=D, num_pages=pages, page_size=page, table_width=page_table.shape[1],
-                 dtype=_dtype(new, "q or k"), k_cache=k_cache.data_ptr(), v_cache=v_cache.data_ptr(),
-                 page_table=page_table.data_ptr(), cu_q=cu_q.data_ptr(), kv_len=kv_len.data_ptr())
+_CACHE = ("pages", "page_size", "Hkv", "D")
 
 
 def paged_append(k, v, k_cache, v_cache, page_table, cu_q, kv_len) -> None:
     """Writes the new tokens' keys and values (k, v [N,Hkv,D]; sequence b's are rows cu_q[b] ..
     cu_q[b+1]-1) to places kv_len[b] - n_b .. kv_len[b] - 1 of the caches [pages, page_size, Hkv, D],
     in place. page_table int32 [B, width], cu_q int32 [B+1], kv_len int32 [B] (new tokens included)."""
-    _dtype(k, "k")
-    _need(k, "k")
-    a = _cache_args(_lib.PagedAppendArgs(), k, k_cache, v_cache, page_table, cu_q, kv_len)
-    _need(k, "k", shape=(k.shape[0], a.Hkv, a.D))
-    _need(v, "v", k.dtype, k.shape)
-    _same_device(k.device, v=v)
-    a.k, a.v = k.data_ptr(), v.data_ptr()
-    _call(_lib.load().rsm_paged_append, a, k.device)
+    dtype, shape, index = _first(k, "k", ("N", "Hkv", "D"))
+    cshape = _first(k_cache, "k_cache", _CACHE)[1]
+    pages, page, Hkv, D = cshape
+    N = shape[0]
+    B, width = _table(page_table)
+    shape = torch.Size((N, Hkv, D))
+    a = _lib.PagedAppendArgs(B, N, Hkv, D, pages, page, width, _DTYPES[dtype], _ptr(k, "k", dtype, shape, index),
+                             _given(v, "v", dtype, shape, index), _ptr(k_cache, "k_cache", dtype, cshape, index),
+                             _given(v_cache, "v_cache", dtype, cshape, index), *_places(page_table, cu_q, kv_len, B, width, index))
+    _run(_lib.load().rsm_paged_append, a, index)
+
+
+def _table(page_table):
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+        raise ValueError("page_table must be a CUDA tensor [B, width]")
+    return page_table.shape
+
+
+def _places(page_table, cu_q, kv_len, B, width, index):
+    i32 = torch.int32
+    return (_ptr(page_table, "page_table", i32, page_table.shape, index), _given(cu_q, "cu_q", i32, torch.Size((B + 1,)), index),
+            _given(kv_len, "kv_len", i32, torch.Size((B,)), index))
 
 
 def paged_forward(q, k_cache, v_cache, page_table, cu_q, kv_len, max_q: int, *, window: int = 0, sinks: int = 0,
@@ -207,54 +210,46 @@ def paged_forward(q, k_cache, v_cache, page_table, cu_q, kv_len, max_q: int, *, 
 
     Returns dict(o [N,H,D] in q's dtype, lse [N,H] fp32 or None); a row that sees nothing gets zeros.
     device_status() reports pages and lengths outside the cache."""
-    _dtype(q, "q")
-    _need(q, "q")
-    if q.dim() != 3:
-        raise ValueError(f"q must be [N,H,D], got {tuple(q.shape)}")
-    a = _cache_args(_lib.PagedArgs(), q, k_cache, v_cache, page_table, cu_q, kv_len)
-    N, H, D = q.shape
-    _need(q, "q", shape=(N, H, a.D))
-    out = out or {}
-    o, ls = out.get("o"), out.get("lse")
+    dtype, shape, index = _first(q, "q", "NHD")
+    cshape = _first(k_cache, "k_cache", _CACHE)[1]
+    pages, page, Hkv, D = cshape
+    N, H, _ = shape
+    B, width = _table(page_table)
+    qp = _ptr(q, "q", dtype, torch.Size((N, H, D)), index)
+    o = ls = None
+    if out:
+        o, ls = out.get("o"), out.get("lse")
     if o is None:
         o = torch.empty_like(q)
-    else:
-        _need(o, "o", q.dtype, q.shape)
-    if ls is not None:
-        _need(ls, "lse", torch.float32, (N, H))
-    elif lse:
+    if ls is None and lse:
         ls = torch.empty(N, H, dtype=torch.float32, device=q.device)
-    _same_device(q.device, o=o, lse=ls)
-    _fill(a, max_q=int(max_q), H=H, window=min(int(window), 2**31 - 1), sinks=min(int(sinks), 2**31 - 1),
-          scale=_scale(scale, D), q=q.data_ptr(), o=o.data_ptr(), lse=_ptr(ls),
-          flags=_lib.RSM_FLAG_VALIDATE if validate else 0)
+    a = _lib.PagedArgs(B, N, _int(max_q), H, Hkv, D, pages, page, width, _int(window), _int(sinks), _DTYPES[dtype],
+                       _scale(scale, D), qp, _ptr(k_cache, "k_cache", dtype, cshape, index),
+                       _given(v_cache, "v_cache", dtype, cshape, index), *_places(page_table, cu_q, kv_len, B, width, index),
+                       _ptr(o, "o", dtype, shape, index), _ptr(ls, "lse", torch.float32, shape[:2], index))
+    if validate:
+        a.flags = _lib.RSM_FLAG_VALIDATE
     L = _lib.load()
-    ws = _workspace(L.rsm_paged_workspace_size, L.rsm_paged_forward, a, q.device, workspace)
-    _call(L.rsm_paged_forward, a, q.device)
-    del ws
+    _run(L.rsm_paged_forward, a, index, L.rsm_paged_workspace_size, workspace)
     return {"o": o, "lse": ls}
 
 
 # ----------------------------------------------------------------------------------- block norms
-def _norm_args(a, y, gate, residual, w_post, w_pre, act, scale, eps):
-    dt = _dtype(residual, "residual")
-    _need(residual, "residual")
-    if residual.dim() < 1:
+def _norm_args(cls, y, gate, residual, w_post, w_pre, act, scale, eps):
+    dtype, shape, index = _first(residual, "residual", None)
+    if not shape:
         raise ValueError("residual must have at least one dimension")
-    d = residual.shape[-1]
-    ty = _dtype(y, "y")
-    _need(y, "y", shape=residual.shape)
-    if gate is not None:
-        _need(gate, "gate", residual.dtype, residual.shape)
-    _need(w_post, "w_post", torch.float32, (d,))
-    if w_pre is not None:
-        _need(w_pre, "w_pre", torch.float32, (d,))
-    if act not in _ACTS:
+    d = shape[-1]
+    ty = _first(y, "y", None)[0]
+    code = _ACTS.get(act)
+    if code is None:
         raise ValueError(f"act must be one of {sorted(_ACTS)}, got {act!r}")
-    _same_device(residual.device, y=y, gate=gate, w_post=w_post, w_pre=w_pre)
-    return _fill(a, rows=residual.numel() // d if d else 0, d=d, y_dtype=ty, dtype=dt, act=_ACTS[act],
-                 scale=float(scale), eps=float(eps), y=y.data_ptr(), gate=_ptr(gate), residual=residual.data_ptr(),
-                 w_post=w_post.data_ptr(), w_pre=_ptr(w_pre))
+    w = torch.Size((d,))
+    a = cls(residual.numel() // d if d else 0, d, _DTYPES[ty], _DTYPES[dtype], code, float(scale), float(eps),
+            _ptr(y, "y", ty, shape, index), _ptr(gate, "gate", dtype, shape, index),
+            _ptr(residual, "residual", dtype, shape, index), _given(w_post, "w_post", torch.float32, w, index),
+            _ptr(w_pre, "w_pre", torch.float32, w, index))
+    return a, dtype, shape, index
 
 
 def block_norm_forward(y, gate, residual, w_post, w_pre=None, *, act: str = "silu", scale: float = 1.0,
@@ -262,22 +257,18 @@ def block_norm_forward(y, gate, residual, w_post, w_pre=None, *, act: str = "sil
     """h = residual + scale rmsnorm(y) w_post act(gate) and x = rmsnorm(h) w_pre over the last axis d.
     y is float32 or of residual's dtype; gate may be None; w_post, w_pre are float32 [d]; without w_pre
     there is no x. Returns dict(h, x) in residual's dtype. `out` may supply them."""
-    a = _norm_args(_lib.BlockNormArgs(), y, gate, residual, w_post, w_pre, act, scale, eps)
-    out = out or {}
-    h, x = out.get("h"), out.get("x")
+    a, dtype, shape, index = _norm_args(_lib.BlockNormArgs, y, gate, residual, w_post, w_pre, act, scale, eps)
+    h = x = None
+    if out:
+        h, x = out.get("h"), out.get("x")
     if h is None:
         h = torch.empty_like(residual)
-    else:
-        _need(h, "h", residual.dtype, residual.shape)
     if w_pre is None:
         x = None
     elif x is None:
         x = torch.empty_like(residual)
-    else:
-        _need(x, "x", residual.dtype, residual.shape)
-    _same_device(residual.device, h=h, x=x)
-    a.h, a.x = h.data_ptr(), _ptr(x)
-    _call(_lib.load().rsm_block_norm_forward, a, residual.device)
+    a.h, a.x = _ptr(h, "h", dtype, shape, index), _ptr(x, "x", dtype, shape, index)
+    _run(_lib.load().rsm_block_norm_forward, a, index)
     return {"h": h, "x": x}
 
 
@@ -286,27 +277,21 @@ def block_norm_backward(y, gate, residual, w_post, w_pre=None, dh=None, dx=None,
                         workspace=None):
     """Gradients of block_norm_forward from dh and dx (residual's dtype; None = zero). Returns dict(dy,
     dgate, dresidual, dw_post, dw_pre), None where there is no input or `need` says so."""
-    a = _norm_args(_lib.BlockNormBackwardArgs(), y, gate, residual, w_post, w_pre, act, scale, eps)
-    for name, t in (("dh", dh), ("dx", dx)):
-        if t is not None:
-            _need(t, name, residual.dtype, residual.shape)
-            setattr(a, name, t.data_ptr())
-    out = dict(out or {})
+    a, dtype, shape, index = _norm_args(_lib.BlockNormBackwardArgs, y, gate, residual, w_post, w_pre, act, scale, eps)
+    a.dh, a.dx = _ptr(dh, "dh", dtype, shape, index), _ptr(dx, "dx", dtype, shape, index)
+    got = {}
     for name, like, wanted in zip(("dy", "dgate", "dresidual", "dw_post", "dw_pre"), (y, gate, residual, w_post, w_pre),
                                   need):
-        if not wanted or like is None:
-            out[name] = None
-            continue
-        if out.get(name) is None:
-            out[name] = torch.empty_like(like)
-        _need(out[name], name, like.dtype, like.shape)
-        setattr(a, name, out[name].data_ptr())
-    _same_device(residual.device, dh=dh, dx=dx, **out)
+        g = None
+        if wanted and like is not None:
+            g = out.get(name) if out else None
+            if g is None:
+                g = torch.empty_like(like)
+            setattr(a, name, _ptr(g, name, like.dtype, like.shape, index))
+        got[name] = g
     L = _lib.load()
-    ws = _workspace(L.rsm_block_norm_backward_workspace_size, L.rsm_block_norm_backward, a, residual.device, workspace)
-    _call(L.rsm_block_norm_backward, a, residual.device)
-    del ws
-    return out
+    _run(L.rsm_block_norm_backward, a, index, L.rsm_block_norm_backward_workspace_size, workspace)
+    return got
 
 
 class BlockNormFunction(torch.autograd.Function):

@@ -88,22 +88,32 @@ template <int NV> RSM_DEV void row_sum(float (&v)[NV], int tpr, float* buf) {
   for (int k = 0; k < NV; ++k) v[k] = warp_sum_f(lane < nw ? buf[k * 32 + w0 + lane] : 0.f);
 }
 
-// The sigmoid from the fast exponential and division (a few ulp each, far below what the row sums and the
-// stored types keep): with the exact ones the instructions, not the memory, set the pace. A gate of -100
-// gives 1 / inf = 0.
-RSM_DEV void activation(rsm_act act, float g, float& a, float& slope) {
-  const float s = __fdividef(1.f, 1.f + __expf(-g));
-  if (act == RSM_ACT_SILU) {
-    a = g * s;
-    slope = s * (1.f + g * (1.f - s));
+// The gate is a template argument: a test per element would cost as much as the arithmetic.
+enum { kNoGate = 0, kSilu = 1, kSigmoid = 2 };
+
+// act(g) and act'(g). The sigmoid is 1 / (1 + 2^(-g log2 e)) from the approximate exponential and reciprocal
+// (2^-22 each, far below what the row sums and the stored types keep): with the exact ones the
+// instructions, not the memory, set the pace. A gate of -100 gives 1 / inf = 0.
+template <int GATE> RSM_DEV void activation(float g, float& a, float& slope) {
+  if constexpr (GATE == kNoGate) {
+    a = 1.f;
+    slope = 0.f;
   } else {
-    a = s;
-    slope = s * (1.f - s);
+    float e, s;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + e));
+    if constexpr (GATE == kSilu) {
+      a = g * s;
+      slope = fmaf(a, 1.f - s, s);
+    } else {
+      a = s;
+      slope = s * (1.f - s);
+    }
   }
 }
 
 // What a thread holds of a row. Rows behind the last one, and columns behind d, are zero.
-template <typename TY, typename T, int VEC, int ITER> struct Row {
+template <typename TY, typename T, int VEC, int ITER, bool GATED> struct Row {
   Raw<TY, VEC> y[ITER];
   Raw<T, VEC> g[ITER], r[ITER];
   template <class A> RSM_DEV void load(const A& a, int64_t row, int t, int tpr) {
@@ -114,7 +124,7 @@ template <typename TY, typename T, int VEC, int ITER> struct Row {
       if (row < a.rows && c < a.d) {
         const int64_t at = row * a.d + c;
         y[i].load(static_cast<const TY*>(a.y) + at);
-        if (a.gate) g[i].load(static_cast<const T*>(a.gate) + at);
+        if (GATED) g[i].load(static_cast<const T*>(a.gate) + at);
         r[i].load(static_cast<const T*>(a.residual) + at);
       }
     }
@@ -139,7 +149,7 @@ template <typename T, int VEC, int ITER> struct Grads {
 // The blocks stay and take row after row. Where a row is one piece per thread (ITER = 1) the next row is on
 // its way while this one is summed up and written: without that, the memory idles during the two row sums
 // (32768 rows of 2048, fp32 y: 236 us against 123 at the copy's rate).
-template <typename TY, typename T, int VEC, int ITER, int THREADS>
+template <typename TY, typename T, int VEC, int ITER, int THREADS, int GATE>
 __global__ void __launch_bounds__(THREADS, ITER == 1 ? 768 / THREADS : 1) block_norm_kernel(const rsm_block_norm_args a, int tpr) {
   __shared__ float buf[2][32];
   const int rpb = blockDim.x / tpr;
@@ -156,12 +166,12 @@ __global__ void __launch_bounds__(THREADS, ITER == 1 ? 768 / THREADS : 1) block_
       if (a.w_pre) w2[i].load(a.w_pre + c);
     }
   }
-  Row<TY, T, VEC, ITER> next;
+  Row<TY, T, VEC, ITER, GATE != kNoGate> next;
   int64_t row = (int64_t)blockIdx.x * rpb + threadIdx.x / tpr;
   if (ITER == 1) next.load(a, row, t, tpr);
   // (every thread of the block makes the same number of rounds: the sums hold barriers)
   for (int64_t row0 = (int64_t)blockIdx.x * rpb; row0 < a.rows; row0 += step, row += step) {
-    Row<TY, T, VEC, ITER> in;
+    Row<TY, T, VEC, ITER, GATE != kNoGate> in;
     if (ITER == 1) {
       in = next;
       next.load(a, row + step, t, tpr);
@@ -184,8 +194,8 @@ __global__ void __launch_bounds__(THREADS, ITER == 1 ? 768 / THREADS : 1) block_
       const int c = (t + i * tpr) * VEC;
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
-        float act = 1.f, slope;
-        if (a.gate) activation(a.act, in.g[i][j], act, slope);
+        float act, slope;
+        activation<GATE>(in.g[i][j], act, slope);
         h[i][j] = fmaf(a.scale * (in.y[i][j] * r1 * w1[i][j]), act, in.r[i][j]);
         sum[0] = fmaf(h[i][j], h[i][j], sum[0]);
       }
@@ -207,7 +217,7 @@ __global__ void __launch_bounds__(THREADS, ITER == 1 ? 768 / THREADS : 1) block_
   }
 }
 
-template <typename TY, typename T, int VEC, int ITER, int THREADS>
+template <typename TY, typename T, int VEC, int ITER, int THREADS, int GATE>
 __global__ void __launch_bounds__(THREADS, 512 / THREADS) block_norm_backward_kernel(const rsm_block_norm_backward_args a, int tpr) {
   __shared__ float buf[2][2][32];
   extern __shared__ float sums[];  // [rpb][2][d]: joins the rows of a block, rpb > 1 only
@@ -228,7 +238,7 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) block_norm_backward_ke
       if (a.w_pre) w2[i].load(a.w_pre + c);
     }
   }
-  Row<TY, T, VEC, ITER> next;
+  Row<TY, T, VEC, ITER, GATE != kNoGate> next;
   Grads<T, VEC, ITER> next_d;
   int64_t row = (int64_t)blockIdx.x * rpb + sub;
   if (ITER == 1) {
@@ -236,7 +246,7 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) block_norm_backward_ke
     next_d.load(a, row, t, tpr);
   }
   for (int64_t row0 = (int64_t)blockIdx.x * rpb; row0 < a.rows; row0 += step, row += step) {
-    Row<TY, T, VEC, ITER> in;
+    Row<TY, T, VEC, ITER, GATE != kNoGate> in;
     Grads<T, VEC, ITER> d;
     if (ITER == 1) {
       in = next;
@@ -262,8 +272,8 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) block_norm_backward_ke
     for (int i = 0; i < ITER; ++i)
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
-        float act = 1.f, slope;
-        if (a.gate) activation(a.act, in.g[i][j], act, slope);
+        float act, slope;
+        activation<GATE>(in.g[i][j], act, slope);
         h[i][j] = fmaf(a.scale * (in.y[i][j] * r1 * w1[i][j]), act, in.r[i][j]);
         two[0] = fmaf(h[i][j], h[i][j], two[0]);
         two[1] = fmaf(d.dx[i][j] * w2[i][j], h[i][j], two[1]);
@@ -278,8 +288,8 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) block_norm_backward_ke
       float dg[VEC], dH[VEC];
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
-        float act = 1.f, slope = 0.f;
-        if (a.gate) activation(a.act, in.g[i][j], act, slope);
+        float act, slope;
+        activation<GATE>(in.g[i][j], act, slope);
         s2[i][j] = fmaf(d.dx[i][j] * h[i][j], r2, s2[i][j]);
         dH[j] = d.dh[i][j] + (r2 * (d.dx[i][j] * w2[i][j]) - h[i][j] * k2);
         const float du = a.scale * dH[j];
@@ -291,7 +301,7 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) block_norm_backward_ke
       }
       if (live && c < a.d) {
         if (a.dresidual) store_vec<T, VEC>(static_cast<T*>(a.dresidual) + base + c, dH);
-        if (a.dgate) store_vec<T, VEC>(static_cast<T*>(a.dgate) + base + c, dg);
+        if (GATE != kNoGate && a.dgate) store_vec<T, VEC>(static_cast<T*>(a.dgate) + base + c, dg);
       }
     }
     row_sum(one, tpr, buf[0][1]);
@@ -375,13 +385,31 @@ int backward_blocks(int64_t rows, const Shape& s) {
   return (int)std::min<int64_t>(need, (int64_t)(512 / s.threads) * device_sm_count());
 }
 
+template <class A> int gate_of(const A& a) { return !a.gate ? kNoGate : a.act == RSM_ACT_SILU ? kSilu : kSigmoid; }
+
+// Calls f with the block size and the gate as compile-time constants. (Rows of more than one piece per
+// thread always take the larger block.)
+template <int ITER, class F> void with_constants(int threads, int gate, F f) {
+  auto gated = [&](auto t) {
+    if (gate == kNoGate) f(t, std::integral_constant<int, kNoGate>());
+    else if (gate == kSilu) f(t, std::integral_constant<int, kSilu>());
+    else f(t, std::integral_constant<int, kSigmoid>());
+  };
+  if constexpr (ITER == 1) {
+    if (threads == 256) return gated(std::integral_constant<int, 256>());
+  }
+  gated(std::integral_constant<int, 512>());
+}
+
 template <typename TY, typename T, int VEC, int ITER>
 cudaError_t forward_as(const rsm_block_norm_args& a, const Shape& s, cudaStream_t stream) {
   const int rpb = s.threads / s.tpr;
   const int64_t need = (a.rows + rpb - 1) / rpb;
   const int64_t grid = std::min<int64_t>(need, (int64_t)(768 / s.threads) * device_sm_count());
-  if (s.threads == 256) block_norm_kernel<TY, T, VEC, ITER, 256><<<(unsigned)grid, 256, 0, stream>>>(a, s.tpr);
-  else block_norm_kernel<TY, T, VEC, ITER, 512><<<(unsigned)grid, 512, 0, stream>>>(a, s.tpr);
+  with_constants<ITER>(s.threads, gate_of(a), [&](auto threads, auto gate) {
+    block_norm_kernel<TY, T, VEC, ITER, decltype(threads)::value, decltype(gate)::value>
+        <<<(unsigned)grid, s.threads, 0, stream>>>(a, s.tpr);
+  });
   return cudaGetLastError();
 }
 
@@ -390,8 +418,10 @@ cudaError_t backward_as(const rsm_block_norm_backward_args& a, const Shape& s, c
   const int rpb = s.threads / s.tpr;
   const int bytes = rpb > 1 ? rpb * 2 * a.d * 4 : 0;  // at most 8 * 2 * 256 * 4
   const int grid = backward_blocks(a.rows, s);
-  if (s.threads == 256) block_norm_backward_kernel<TY, T, VEC, ITER, 256><<<grid, 256, bytes, stream>>>(a, s.tpr);
-  else block_norm_backward_kernel<TY, T, VEC, ITER, 512><<<grid, 512, bytes, stream>>>(a, s.tpr);
+  with_constants<ITER>(s.threads, gate_of(a), [&](auto threads, auto gate) {
+    block_norm_backward_kernel<TY, T, VEC, ITER, decltype(threads)::value, decltype(gate)::value>
+        <<<grid, s.threads, bytes, stream>>>(a, s.tpr);
+  });
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !(a.dw_post || a.dw_pre)) return e;
   weight_sum_kernel<<<(2 * a.d + 31) / 32, 256, 0, stream>>>(static_cast<const float*>(a.workspace), grid, a.d,

@@ -73,15 +73,6 @@ RSM_DEV int window_last(int k1, int T, int window, int tok_tile) {
   return (int)((min((int64_t)T, (int64_t)k1 + window) - 1) / tok_tile);
 }
 
-RSM_DEV float2 mul2(float2 a, float2 b) {
-  float2 d;
-  asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
-      "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
-
 // ntiles: dq: query tiles of 128 rows per pair; otherwise query tiles of 64 rows (the statistics').
 template <int DP, bool DQ>
 __global__ void __launch_bounds__(kThreads, 1) attn_tc_backward_kernel(const __grid_constant__ Maps maps, const AttnParams p,

@@ -7,7 +7,7 @@
 //   dH = dh + r2 e - h r2^3 mean(e h),  dres = dH,  du = scale dH
 //   dg = du n act'(g),  f = du act(g) w_post,  dy = r1 f - y r1^3 mean(f y)
 //   dw_post = sum_rows du act(g) y r1,  dw_pre = sum_rows dx h r2
-// Everything is fp32 between the loads and the stores; h is normalised before it is rounded, and the
+// Everything is fp32, two values per instruction, between the loads and the stores; h is normalised before it is rounded, and the
 // backward forms it again from its inputs, so no rounded value enters a sum.
 //
 // A row stays in registers: TPR threads hold VEC * ITER values each, and the row crosses memory once
@@ -47,45 +47,57 @@ template <typename T, int VEC> struct Raw {
       }
     }
   }
-  RSM_DEV float operator[](int i) const {
-    if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
-    else return __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
+  // values 2 i and 2 i + 1
+  RSM_DEV float2 operator[](int i) const {
+    if constexpr (sizeof(T) == 4) return make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+    else return make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
   }
 };
 
-template <typename T, int VEC> RSM_DEV void store_vec(T* p, const float (&x)[VEC]) {
+template <typename T, int VEC> RSM_DEV void store_vec(T* p, const float2 (&x)[VEC / 2]) {
   if constexpr (sizeof(T) == 2) {
     uint32_t w[VEC / 2];
 #pragma unroll
     for (int i = 0; i < VEC / 2; ++i) {
-      const __nv_bfloat162 t = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+      const __nv_bfloat162 t = __floats2bfloat162_rn(x[i].x, x[i].y);
       w[i] = *reinterpret_cast<const uint32_t*>(&t);
     }
     if constexpr (VEC == 8) *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
     else *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
   } else {
 #pragma unroll
-    for (int i = 0; i < VEC; i += 4)
-      *reinterpret_cast<float4*>(p + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+    for (int i = 0; i < VEC / 2; i += 2)
+      *reinterpret_cast<float4*>(p + 2 * i) = make_float4(x[i].x, x[i].y, x[i + 1].x, x[i + 1].y);
   }
 }
 
 // Sums of NV values over the TPR threads of a row (TPR a multiple of 32; every thread of the block
 // calls it). `buf` holds one value per warp and NV; successive calls alternate between two buffers,
-// so one barrier per call is enough.
-template <int NV> RSM_DEV void row_sum(float (&v)[NV], int tpr, float* buf) {
+// so one barrier per call is enough. The second stage reads the warps' sums four at a time.
+template <int NV> RSM_DEV void row_sum(float (&v)[NV], int tpr, float (*buf)[32]) {
 #pragma unroll
   for (int k = 0; k < NV; ++k) v[k] = warp_sum_f(v[k]);
   if (tpr == 32) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (lane == 0) {
 #pragma unroll
-    for (int k = 0; k < NV; ++k) buf[k * 32 + warp] = v[k];
+    for (int k = 0; k < NV; ++k) buf[k][warp] = v[k];
   }
   __syncthreads();
-  const int nw = tpr >> 5, w0 = warp / nw * nw;
+  const int nw = tpr >> 5, w0 = warp & ~(nw - 1);  // (nw is a power of two, 2 to 16)
 #pragma unroll
-  for (int k = 0; k < NV; ++k) v[k] = warp_sum_f(lane < nw ? buf[k * 32 + w0 + lane] : 0.f);
+  for (int k = 0; k < NV; ++k) {
+    if (nw == 2) {
+      v[k] = buf[k][w0] + buf[k][w0 + 1];
+    } else {
+      float4 s = *reinterpret_cast<const float4*>(&buf[k][w0]);
+      for (int w = 4; w < nw; w += 4) {
+        const float4 t = *reinterpret_cast<const float4*>(&buf[k][w0 + w]);
+        s.x += t.x; s.y += t.y; s.z += t.z; s.w += t.w;
+      }
+      v[k] = (s.x + s.y) + (s.z + s.w);
+    }
+  }
 }
 
 // The gate is a template argument: a test per element would cost as much as the arithmetic.
@@ -94,20 +106,25 @@ enum { kNoGate = 0, kSilu = 1, kSigmoid = 2 };
 // act(g) and act'(g). The sigmoid is 1 / (1 + 2^(-g log2 e)) from the approximate exponential and reciprocal
 // (2^-22 each, far below what the row sums and the stored types keep): with the exact ones the
 // instructions, not the memory, set the pace. A gate of -100 gives 1 / inf = 0.
-template <int GATE> RSM_DEV void activation(float g, float& a, float& slope) {
+template <int GATE> RSM_DEV void activation(float2 g, float2& a, float2& slope) {
   if constexpr (GATE == kNoGate) {
-    a = 1.f;
-    slope = 0.f;
+    a = both(1.f);
+    slope = both(0.f);
   } else {
-    float e, s;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + e));
+    const float2 z = mul2(g, both(-1.4426950408889634f));
+    float2 e, s;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(z.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(z.y));
+    e = add2(e, both(1.f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.x) : "f"(e.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.y) : "f"(e.y));
+    const float2 rest = fma2(s, both(-1.f), both(1.f));
     if constexpr (GATE == kSilu) {
-      a = g * s;
-      slope = fmaf(a, 1.f - s, s);
+      a = mul2(g, s);
+      slope = fma2(a, rest, s);
     } else {
       a = s;
-      slope = s * (1.f - s);
+      slope = mul2(s, rest);
     }
   }
 }
@@ -151,7 +168,7 @@ template <typename T, int VEC, int ITER> struct Grads {
 // (32768 rows of 2048, fp32 y: 236 us against 123 at the copy's rate).
 template <typename TY, typename T, int VEC, int ITER, int THREADS, int GATE>
 __global__ void __launch_bounds__(THREADS, ITER == 1 ? 768 / THREADS : 1) block_norm_kernel(const rsm_block_norm_args a, int tpr) {
-  __shared__ float buf[2][32];
+  __shared__ __align__(16) float buf[2][32];
   const int rpb = blockDim.x / tpr;
   const int t = threadIdx.x % tpr;
   const int64_t step = (int64_t)gridDim.x * rpb;
@@ -180,35 +197,37 @@ __global__ void __launch_bounds__(THREADS, ITER == 1 ? 768 / THREADS : 1) block_
     }
     const bool live = row < a.rows;
     const int64_t base = row * a.d;
-    float sum[1] = {0.f};
+    float2 acc = both(0.f);
 #pragma unroll
     for (int i = 0; i < ITER; ++i)
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) sum[0] = fmaf(in.y[i][j], in.y[i][j], sum[0]);
-    row_sum(sum, tpr, buf[0]);
-    const float r1 = rsqrtf(sum[0] * inv_d + a.eps);
-    sum[0] = 0.f;
-    float h[ITER][VEC];
+      for (int j = 0; j < VEC / 2; ++j) acc = fma2(in.y[i][j], in.y[i][j], acc);
+    float sum[1] = {acc.x + acc.y};
+    row_sum(sum, tpr, &buf[0]);
+    const float2 r1 = both(a.scale * rsqrtf(sum[0] * inv_d + a.eps));
+    acc = both(0.f);
+    float2 h[ITER][VEC / 2];
 #pragma unroll
     for (int i = 0; i < ITER; ++i) {
       const int c = (t + i * tpr) * VEC;
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        float act, slope;
+      for (int j = 0; j < VEC / 2; ++j) {
+        float2 act, slope;
         activation<GATE>(in.g[i][j], act, slope);
-        h[i][j] = fmaf(a.scale * (in.y[i][j] * r1 * w1[i][j]), act, in.r[i][j]);
-        sum[0] = fmaf(h[i][j], h[i][j], sum[0]);
+        h[i][j] = fma2(mul2(mul2(in.y[i][j], r1), w1[i][j]), act, in.r[i][j]);
+        acc = fma2(h[i][j], h[i][j], acc);
       }
       if (live && c < a.d) store_vec<T, VEC>(static_cast<T*>(a.h) + base + c, h[i]);
     }
     if (a.w_pre) {
-      row_sum(sum, tpr, buf[1]);
-      const float r2 = rsqrtf(sum[0] * inv_d + a.eps);
+      sum[0] = acc.x + acc.y;
+      row_sum(sum, tpr, &buf[1]);
+      const float2 r2 = both(rsqrtf(sum[0] * inv_d + a.eps));
 #pragma unroll
       for (int i = 0; i < ITER; ++i) {
         const int c = (t + i * tpr) * VEC;
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) h[i][j] = h[i][j] * r2 * w2[i][j];
+        for (int j = 0; j < VEC / 2; ++j) h[i][j] = mul2(mul2(h[i][j], r2), w2[i][j]);
         if (live && c < a.d) store_vec<T, VEC>(static_cast<T*>(a.x) + base + c, h[i]);
       }
     } else {
@@ -218,21 +237,22 @@ __global__ void __launch_bounds__(THREADS, ITER == 1 ? 768 / THREADS : 1) block_
 }
 
 template <typename TY, typename T, int VEC, int ITER, int THREADS, int GATE>
-__global__ void __launch_bounds__(THREADS, 512 / THREADS) block_norm_backward_kernel(const rsm_block_norm_backward_args a, int tpr) {
-  __shared__ float buf[2][2][32];
+__global__ void __launch_bounds__(THREADS, 512 / THREADS)
+    block_norm_backward_kernel(const rsm_block_norm_backward_args a, int tpr) {
+  __shared__ __align__(16) float buf[2][2][32];
   extern __shared__ float sums[];  // [rpb][2][d]: joins the rows of a block, rpb > 1 only
   const int rpb = blockDim.x / tpr;
   const int sub = threadIdx.x / tpr, t = threadIdx.x % tpr;
   const int64_t step = (int64_t)gridDim.x * rpb;
   const float inv_d = 1.f / (float)a.d;
   Raw<float, VEC> w1[ITER], w2[ITER];
-  float s1[ITER][VEC], s2[ITER][VEC];
+  float2 s1[ITER][VEC / 2], s2[ITER][VEC / 2];
 #pragma unroll
   for (int i = 0; i < ITER; ++i) {
     const int c = (t + i * tpr) * VEC;
     w1[i].zero(); w2[i].zero();
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) s1[i][j] = s2[i][j] = 0.f;
+    for (int j = 0; j < VEC / 2; ++j) s1[i][j] = s2[i][j] = both(0.f);
     if (c < a.d) {
       w1[i].load(a.w_post + c);
       if (a.w_pre) w2[i].load(a.w_pre + c);
@@ -259,59 +279,63 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) block_norm_backward_ke
     }
     const bool live = row < a.rows;
     const int64_t base = row * a.d;
-    float one[1] = {0.f};
+    float2 acc = both(0.f);
 #pragma unroll
     for (int i = 0; i < ITER; ++i)
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) one[0] = fmaf(in.y[i][j], in.y[i][j], one[0]);
-    row_sum(one, tpr, buf[0][0]);
-    const float r1 = rsqrtf(one[0] * inv_d + a.eps);
-    float two[2] = {0.f, 0.f};
-    float h[ITER][VEC];
+      for (int j = 0; j < VEC / 2; ++j) acc = fma2(in.y[i][j], in.y[i][j], acc);
+    float one[1] = {acc.x + acc.y};
+    row_sum(one, tpr, &buf[0][0]);
+    const float rs1 = rsqrtf(one[0] * inv_d + a.eps);
+    const float2 r1 = both(rs1), r1s = both(a.scale * rs1);
+    float2 acc2 = acc = both(0.f);
+    float2 h[ITER][VEC / 2];
 #pragma unroll
     for (int i = 0; i < ITER; ++i)
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        float act, slope;
+      for (int j = 0; j < VEC / 2; ++j) {
+        float2 act, slope;
         activation<GATE>(in.g[i][j], act, slope);
-        h[i][j] = fmaf(a.scale * (in.y[i][j] * r1 * w1[i][j]), act, in.r[i][j]);
-        two[0] = fmaf(h[i][j], h[i][j], two[0]);
-        two[1] = fmaf(d.dx[i][j] * w2[i][j], h[i][j], two[1]);
+        h[i][j] = fma2(mul2(mul2(in.y[i][j], r1s), w1[i][j]), act, in.r[i][j]);
+        acc = fma2(h[i][j], h[i][j], acc);
+        acc2 = fma2(mul2(d.dx[i][j], w2[i][j]), h[i][j], acc2);
       }
-    row_sum(two, tpr, buf[1][0]);
-    const float r2 = rsqrtf(two[0] * inv_d + a.eps);
-    const float k2 = r2 * r2 * r2 * (two[1] * inv_d);
-    one[0] = 0.f;
+    float two[2] = {acc.x + acc.y, acc2.x + acc2.y};
+    row_sum(two, tpr, &buf[1][0]);
+    const float rs2 = rsqrtf(two[0] * inv_d + a.eps);
+    const float2 r2 = both(rs2), k2 = both(-rs2 * rs2 * rs2 * (two[1] * inv_d)), al = both(a.scale);
+    acc = both(0.f);
 #pragma unroll
     for (int i = 0; i < ITER; ++i) {
       const int c = (t + i * tpr) * VEC;
-      float dg[VEC], dH[VEC];
+      float2 dg[VEC / 2], dH[VEC / 2];
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        float act, slope;
+      for (int j = 0; j < VEC / 2; ++j) {
+        float2 act, slope;
         activation<GATE>(in.g[i][j], act, slope);
-        s2[i][j] = fmaf(d.dx[i][j] * h[i][j], r2, s2[i][j]);
-        dH[j] = d.dh[i][j] + (r2 * (d.dx[i][j] * w2[i][j]) - h[i][j] * k2);
-        const float du = a.scale * dH[j];
-        const float yr = in.y[i][j] * r1;
-        dg[j] = du * (yr * w1[i][j]) * slope;
-        s1[i][j] = fmaf(du * act, yr, s1[i][j]);
-        h[i][j] = du * act * w1[i][j];  // f
-        one[0] = fmaf(h[i][j], in.y[i][j], one[0]);
+        const float2 dx = d.dx[i][j], y = in.y[i][j];
+        s2[i][j] = fma2(mul2(dx, h[i][j]), r2, s2[i][j]);
+        dH[j] = fma2(h[i][j], k2, fma2(mul2(dx, w2[i][j]), r2, d.dh[i][j]));
+        const float2 du = mul2(dH[j], al), ya = mul2(y, r1), dn = mul2(du, act);
+        if (GATE != kNoGate) dg[j] = mul2(mul2(du, slope), mul2(ya, w1[i][j]));
+        s1[i][j] = fma2(dn, ya, s1[i][j]);
+        h[i][j] = mul2(dn, w1[i][j]);  // f
+        acc = fma2(h[i][j], y, acc);
       }
       if (live && c < a.d) {
         if (a.dresidual) store_vec<T, VEC>(static_cast<T*>(a.dresidual) + base + c, dH);
         if (GATE != kNoGate && a.dgate) store_vec<T, VEC>(static_cast<T*>(a.dgate) + base + c, dg);
       }
     }
-    row_sum(one, tpr, buf[0][1]);
-    const float k1 = r1 * r1 * r1 * (one[0] * inv_d);
+    one[0] = acc.x + acc.y;
+    row_sum(one, tpr, &buf[0][1]);
+    const float2 k1 = both(-rs1 * rs1 * rs1 * (one[0] * inv_d));
     if (a.dy) {
 #pragma unroll
       for (int i = 0; i < ITER; ++i) {
         const int c = (t + i * tpr) * VEC;
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) h[i][j] = r1 * h[i][j] - in.y[i][j] * k1;
+        for (int j = 0; j < VEC / 2; ++j) h[i][j] = fma2(in.y[i][j], k1, mul2(h[i][j], r1));
         if (live && c < a.d) store_vec<TY, VEC>(static_cast<TY*>(a.dy) + base + c, h[i]);
       }
     }
@@ -362,14 +386,14 @@ __global__ void __launch_bounds__(256) weight_sum_kernel(const float* part, int 
   }
 }
 
-// Threads and values per thread for a row of d: 16-byte pieces of `dtype` where the rows allow it, the
-// fewest threads (a power of two, at least a warp) that hold the row in one piece each, at most 512.
+// Threads and values per thread for a row of d: pieces of `vec` values, the fewest threads (a power of two,
+// at least a warp) that hold the row in one piece each, at most 512.
 struct Shape {
   int vec, tpr, iter, threads;
 };
-Shape shape_for(int d, rsm_dtype dtype) {
+Shape shape_of(int d, int vec) {
   Shape s;
-  s.vec = dtype == RSM_BF16 && d % 8 == 0 ? 8 : 4;
+  s.vec = vec;
   const int pieces = d / s.vec;
   s.tpr = 32;
   while (s.tpr < pieces && s.tpr < kMaxThreads) s.tpr *= 2;
@@ -378,7 +402,8 @@ Shape shape_for(int d, rsm_dtype dtype) {
   s.threads = std::max(s.tpr, 256);
   return s;
 }
-
+// 16-byte pieces where the rows allow it
+Shape shape_for(int d, rsm_dtype dtype) { return shape_of(d, dtype == RSM_BF16 && d % 8 == 0 ? 8 : 4); }
 int backward_blocks(int64_t rows, const Shape& s) {
   const int rpb = s.threads / s.tpr;
   const int64_t need = (rows + rpb - 1) / rpb;

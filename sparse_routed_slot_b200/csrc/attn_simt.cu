@@ -44,17 +44,25 @@ template <> struct Out<__nv_bfloat16> {
   }
 };
 
-// Row r of a tile of n rows comes from base + offset(r) (fp32 in shared memory), or is zero where
-// offset(r) < 0. Columns past D are left alone: no product reads them into a column that is stored.
-template <typename T, int DP, class Off>
-RSM_DEV void load_rows(float* dst, const void* base, int n, int D, Off offset) {
-  const int per = D >> 2;
-  for (int e = threadIdx.x; e < n * per; e += kThreads) {
-    const int r = e / per, c = (e - r * per) << 2;
+// Row r of a tile of N rows comes from base + offset(r) (fp32 in shared memory), or is zero where
+// offset(r) < 0. 16 threads share a row, so a row's offset (divisions by the group or page size) is found
+// once per 16 bytes x D / 64 and thread. Columns past D are left alone: no product reads them into a
+// column that is stored. With `used`, it gets whether each row is there.
+template <typename T, int DP, int N, class Off>
+RSM_DEV void load_rows(float* dst, const void* base, int D, int tx, int ty, Off offset, int* used = nullptr) {
+#pragma unroll
+  for (int k = 0; k < N / 16; ++k) {
+    const int r = ty + 16 * k;
     const int64_t off = offset(r);
-    float x[4] = {0.f, 0.f, 0.f, 0.f};
-    if (off >= 0) In<T>::ld4(static_cast<const T*>(base) + off + c, x);
-    *reinterpret_cast<float4*>(dst + r * (DP + 4) + c) = make_float4(x[0], x[1], x[2], x[3]);
+    if (used && tx == 0) used[r] = off >= 0;
+#pragma unroll
+    for (int jj = 0; jj < DP / 64; ++jj) {
+      const int c = 4 * tx + 64 * jj;
+      if (c >= D) continue;
+      float x[4] = {0.f, 0.f, 0.f, 0.f};
+      if (off >= 0) In<T>::ld4(static_cast<const T*>(base) + off + c, x);
+      *reinterpret_cast<float4*>(dst + r * (DP + 4) + c) = make_float4(x[0], x[1], x[2], x[3]);
+    }
   }
 }
 
@@ -127,6 +135,7 @@ template <typename T, int DP>
 __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const AttnParams p, int ntiles) {
   constexpr int BB = Tile<DP>::kBB;
   extern __shared__ float sm[];
+  __shared__ int used[BB];  // keys of the tile that are there
   float* sQ = sm;
   float* sK = sQ + kBA * (DP + 4);
   float* sV = sK + BB * (DP + 4);
@@ -143,9 +152,8 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const AttnParams p,
   if (rows <= 0) return;
   const int G = p.G, D = p.D;
   auto q_index = [&](int r) { return (s.row0 + (r0 + r) / G) * p.H + hk * G + (r0 + r) % G; };
-  load_rows<T, DP>(sQ, p.q, kBA, D, [&](int r) { return r < rows ? q_index(r) * D : (int64_t)-1; });
-
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  load_rows<T, DP, kBA>(sQ, p.q, D, tx, ty, [&](int r) { return r < rows ? q_index(r) * D : (int64_t)-1; });
   int pos[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) pos[i] = s.pos0 + (r0 + ty + 16 * i) / G;
@@ -167,8 +175,8 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const AttnParams p,
     __syncthreads();
     // rows behind the last key are zero, so that a weight of zero meets no stale NaN
     auto off = [&](int r) { return k0 + r < s.kv ? kv_offset(p, b, hk, k0 + r) : (int64_t)-1; };
-    load_rows<T, DP>(sK, p.k, BB, D, off);
-    load_rows<T, DP>(sV, p.v, BB, D, off);
+    load_rows<T, DP, BB>(sK, p.k, D, tx, ty, off, used);
+    load_rows<T, DP, BB>(sV, p.v, D, tx, ty, off);
     __syncthreads();
     float c[4][BB / 16];
     product_nt<DP, BB>(sQ, sK, D, tx, ty, c);
@@ -178,8 +186,7 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const AttnParams p,
 #pragma unroll
       for (int j = 0; j < BB / 16; ++j) {
         const int key = k0 + tx + 16 * j;
-        bool seen = key < s.kv && sees(pos[i], key, p.window, p.sinks);
-        if (seen && p.table) seen = kv_offset(p, b, hk, key) >= 0;
+        const bool seen = used[tx + 16 * j] && sees(pos[i], key, p.window, p.sinks);
         c[i][j] = seen ? c[i][j] * scale2 : kNegInf;
         top = fmaxf(top, c[i][j]);
       }
@@ -228,11 +235,20 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const AttnParams p,
   }
 }
 
+// How the walks of the first key tiles, whose keys every later row sees, are cut: `parts` blocks per tile,
+// each with its share of the query rows, leave fp32 sums that a small kernel adds in order. Uncut, the
+// longest walk is what the kernel ends with (777 tokens, window 128, groups of 2: 413 us of 495).
+struct Cut {
+  int tiles;    // key tiles that are cut
+  int parts;
+  float* part;  // [pairs][tiles][parts][64][2][D]
+};
+
 // Gradients. DQ: the stationary rows are query rows (A1 = q, A2 = dO), the streamed ones keys
 // (B1 = k, B2 = v) and acc2 = dq. Otherwise the stationary rows are keys (k, v), the streamed ones
 // query rows (q, dO), acc1 = dv and acc2 = dk.
 template <typename T, int DP, bool DQ>
-__global__ void __launch_bounds__(kThreads) attn_simt_backward_kernel(const AttnParams p, int ntiles) {
+__global__ void __launch_bounds__(kThreads) attn_simt_backward_kernel(const AttnParams p, int ntiles, Cut cut) {
   constexpr int BB = 32;
   extern __shared__ float sm[];
   float* sA1 = sm;
@@ -242,37 +258,60 @@ __global__ void __launch_bounds__(kThreads) attn_simt_backward_kernel(const Attn
   float* sW2 = sB2 + BB * (DP + 4);
   float* sW1 = sW2 + kBA * (BB + 4);              // DQ: not used
   float* sStat = DQ ? sW1 : sW1 + kBA * (BB + 4);  // lse (base 2) and delta of the query rows
-  const int tile = blockIdx.x % ntiles, pair = blockIdx.x / ntiles;
+  int tile, pair, part = 0;
+  if (DQ) {
+    tile = blockIdx.x % ntiles;
+    pair = blockIdx.x / ntiles;
+  } else {
+    // the cut tiles' parts come first
+    const int items = ntiles + cut.tiles * (cut.parts - 1);
+    const int item = blockIdx.x % items;
+    pair = blockIdx.x / items;
+    const bool is_cut = item < cut.tiles * cut.parts;
+    tile = is_cut ? item / cut.parts : item - cut.tiles * (cut.parts - 1);
+    part = is_cut ? item % cut.parts : 0;
+  }
+  const bool to_part = !DQ && tile < cut.tiles;
   const int hk = pair % p.Hkv, b = pair / p.Hkv;
   const int G = p.G, D = p.D, T_ = p.T;
-  const int64_t nrows = (int64_t)T_ * G;  // packed query rows of this pair (< 2^31)
+  const int nrows = T_ * G;  // packed query rows of this pair
   const int a0 = tile * kBA;
-  auto q_index = [&](int64_t r) { return ((int64_t)b * T_ + r / G) * p.H + hk * G + r % G; };
-  auto q_off = [&](int64_t r) { return r < nrows ? q_index(r) * D : (int64_t)-1; };
+  auto q_index = [&](int r) { return ((int64_t)b * T_ + r / G) * p.H + hk * G + r % G; };
+  auto q_off = [&](int r) { return r < nrows ? q_index(r) * D : (int64_t)-1; };
   auto k_off = [&](int key) { return key < T_ ? kv_offset(p, b, hk, key) : (int64_t)-1; };
-  auto load_stats = [&](int64_t r0, int n) {
+  auto load_stats = [&](int r0, int n) {
     for (int r = threadIdx.x; r < n; r += kThreads) {
       const bool in = r0 + r < nrows;
       sStat[2 * r] = in ? p.lse[q_index(r0 + r)] * kLog2e : 0.f;
       sStat[2 * r + 1] = in ? p.delta[q_index(r0 + r)] : 0.f;
     }
   };
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   Walk walk{0, 0, 0};
+  int w0 = 0, w1;
   if (DQ) {
-    load_rows<T, DP>(sA1, p.q, kBA, D, [&](int r) { return q_off(a0 + r); });
-    load_rows<T, DP>(sA2, p.dO, kBA, D, [&](int r) { return q_off(a0 + r); });
+    load_rows<T, DP, kBA>(sA1, p.q, D, tx, ty, [&](int r) { return q_off(a0 + r); });
+    load_rows<T, DP, kBA>(sA2, p.dO, D, tx, ty, [&](int r) { return q_off(a0 + r); });
     load_stats(a0, kBA);
-    walk = key_walk(a0 / G, (int)(min(nrows, (int64_t)a0 + kBA) - 1) / G, T_, p.window, p.sinks, BB);
+    walk = key_walk(a0 / G, (min(nrows, a0 + kBA) - 1) / G, T_, p.window, p.sinks, BB);
+    w1 = walk.n;
   } else {
-    load_rows<T, DP>(sA1, p.k, kBA, D, [&](int r) { return k_off(a0 + r); });
-    load_rows<T, DP>(sA2, p.v, kBA, D, [&](int r) { return k_off(a0 + r); });
+    load_rows<T, DP, kBA>(sA1, p.k, D, tx, ty, [&](int r) { return k_off(a0 + r); });
+    load_rows<T, DP, kBA>(sA2, p.v, D, tx, ty, [&](int r) { return k_off(a0 + r); });
     int t0, t1;
     query_range(a0, min(a0 + kBA, T_) - 1, T_, p.window, p.sinks, t0, t1);
     walk.first = t0 * G / BB;
-    walk.n = (int)(((int64_t)t1 * G - 1) / BB) + 1 - walk.first;
+    walk.n = (t1 * G - 1) / BB + 1 - walk.first;
+    w1 = walk.n;
+    if (to_part) {
+      w0 = (int)((int64_t)walk.n * part / cut.parts);
+      w1 = (int)((int64_t)walk.n * (part + 1) / cut.parts);
+    }
   }
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const float scale2 = p.scale * kLog2e;
+  int pos[4];  // DQ: the rows' places
+#pragma unroll
+  for (int i = 0; i < 4; ++i) pos[i] = (a0 + ty + 16 * i) / G;
   float4 acc1[DQ ? 1 : 4][DP / 64], acc2[4][DP / 64];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -281,15 +320,15 @@ __global__ void __launch_bounds__(kThreads) attn_simt_backward_kernel(const Attn
       if (!DQ) acc1[DQ ? 0 : i][jj] = make_float4(0.f, 0.f, 0.f, 0.f);
       acc2[i][jj] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
-  for (int w = 0; w < walk.n; ++w) {
+  for (int w = w0; w < w1; ++w) {
     const int b0 = walk.tile(w) * BB;
     __syncthreads();
     if (DQ) {
-      load_rows<T, DP>(sB1, p.k, BB, D, [&](int r) { return k_off(b0 + r); });
-      load_rows<T, DP>(sB2, p.v, BB, D, [&](int r) { return k_off(b0 + r); });
+      load_rows<T, DP, BB>(sB1, p.k, D, tx, ty, [&](int r) { return k_off(b0 + r); });
+      load_rows<T, DP, BB>(sB2, p.v, D, tx, ty, [&](int r) { return k_off(b0 + r); });
     } else {
-      load_rows<T, DP>(sB1, p.q, BB, D, [&](int r) { return q_off(b0 + r); });
-      load_rows<T, DP>(sB2, p.dO, BB, D, [&](int r) { return q_off(b0 + r); });
+      load_rows<T, DP, BB>(sB1, p.q, D, tx, ty, [&](int r) { return q_off(b0 + r); });
+      load_rows<T, DP, BB>(sB2, p.dO, D, tx, ty, [&](int r) { return q_off(b0 + r); });
       load_stats(b0, BB);
     }
     __syncthreads();
@@ -297,14 +336,16 @@ __global__ void __launch_bounds__(kThreads) attn_simt_backward_kernel(const Attn
     product_nt<DP, BB>(sA1, sB1, D, tx, ty, c1);
     product_nt<DP, BB>(sA2, sB2, D, tx, ty, c2);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int j = 0; j < BB / 16; ++j) {
+      const int rb = tx + 16 * j;
+      const int there = DQ ? b0 + rb < T_ : b0 + rb < nrows;
+      const int pos_b = DQ ? 0 : (b0 + rb) / G;
 #pragma unroll
-      for (int j = 0; j < BB / 16; ++j) {
-        const int ra = ty + 16 * i, rb = tx + 16 * j;
-        const int key = DQ ? b0 + rb : a0 + ra;
-        const int row = DQ ? a0 + ra : b0 + rb;
+      for (int i = 0; i < 4; ++i) {
+        const int ra = ty + 16 * i;
+        const bool in_a = DQ ? a0 + ra < nrows : a0 + ra < T_;
         const float* st = sStat + 2 * (DQ ? ra : rb);
-        const bool seen = row < nrows && key < T_ && sees(row / G, key, p.window, p.sinks);
+        const bool seen = there && in_a && (DQ ? sees(pos[i], b0 + rb, p.window, p.sinks) : sees(pos_b, a0 + ra, p.window, p.sinks));
         const float pr = seen ? exp2f(c1[i][j] * scale2 - st[0]) : 0.f;
         const float ds = seen ? pr * (c2[i][j] - st[1]) : 0.f;
         sW2[ra * (BB + 4) + rb] = ds;
@@ -317,22 +358,48 @@ __global__ void __launch_bounds__(kThreads) attn_simt_backward_kernel(const Attn
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int64_t r = a0 + ty + 16 * i;
-    const int64_t off = DQ ? q_off(r) : k_off((int)r);
+    const int r = a0 + ty + 16 * i;
+    const int64_t off = DQ ? q_off(r) : k_off(r);
     if (off < 0) continue;
+    float* sums = to_part ? cut.part + ((((int64_t)pair * cut.tiles + tile) * cut.parts + part) * kBA + ty + 16 * i) * 2 * D : nullptr;
 #pragma unroll
     for (int jj = 0; jj < DP / 64; ++jj) {
       const int d = 4 * tx + 64 * jj;
       if (d >= D) continue;
       const float4 a = acc2[i][jj];
-      T* g = static_cast<T*>(DQ ? p.dq : p.dk);
-      if (g) Out<T>::st4(g + off + d, a.x * p.scale, a.y * p.scale, a.z * p.scale, a.w * p.scale);
-      if (!DQ && p.dv) {
-        const float4 v = acc1[DQ ? 0 : i][jj];
-        Out<T>::st4(static_cast<T*>(p.dv) + off + d, v.x, v.y, v.z, v.w);
+      const float4 k4 = make_float4(a.x * p.scale, a.y * p.scale, a.z * p.scale, a.w * p.scale);
+      const float4 v4 = DQ ? a : acc1[DQ ? 0 : i][jj];
+      if (to_part) {
+        *reinterpret_cast<float4*>(sums + d) = v4;
+        *reinterpret_cast<float4*>(sums + D + d) = k4;
+        continue;
       }
+      T* g = static_cast<T*>(DQ ? p.dq : p.dk);
+      if (g) Out<T>::st4(g + off + d, k4.x, k4.y, k4.z, k4.w);
+      if (!DQ && p.dv) Out<T>::st4(static_cast<T*>(p.dv) + off + d, v4.x, v4.y, v4.z, v4.w);
     }
   }
+}
+
+// Adds the parts of the cut tiles up, in order, 16 bytes of dv or dk per thread.
+template <typename T> __global__ void __launch_bounds__(256) cut_sum_kernel(const AttnParams p, Cut cut) {
+  const int per = p.D / 2;  // pieces of 4 of a row's dv and dk
+  const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int d = (int)(e % per) * 4;
+  const int64_t row = e / per;
+  const int r = (int)(row % kBA), tile = (int)(row / kBA % cut.tiles);
+  const int64_t pair = row / kBA / cut.tiles;
+  const int key = tile * kBA + r;
+  if (pair >= (int64_t)p.B * p.Hkv || key >= p.T) return;
+  const float* part = cut.part + ((pair * cut.tiles + tile) * cut.parts * kBA + r) * 2 * p.D + d;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int c = 0; c < cut.parts; ++c) {
+    const float4 x = *reinterpret_cast<const float4*>(part + (int64_t)c * kBA * 2 * p.D);
+    s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
+  }
+  T* out = static_cast<T*>(d < p.D ? p.dv : p.dk);
+  const int64_t at = (pair / p.Hkv * p.T + key) * p.Hkv + pair % p.Hkv;
+  if (out) Out<T>::st4(out + at * p.D + (d < p.D ? d : d - p.D), s.x, s.y, s.z, s.w);
 }
 
 // delta = dO . o, a warp per row.
@@ -447,19 +514,44 @@ cudaError_t forward_dp(const AttnParams& p, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
+// Tiles whose keys are all behind the sinks are left whole; so is everything where the walk past the window
+// is no longer than the window, or where there are so many sinks that the walks are all alike.
+Cut cut_for(const AttnParams& p) {
+  Cut c{0, 1, nullptr};
+  const int ntiles = (p.T + kBA - 1) / kBA;
+  const int tiles = (std::min(p.sinks, p.T) + kBA - 1) / kBA;
+  const int64_t near = std::min<int64_t>(p.T, (int64_t)kBA + p.window);
+  if (tiles == 0 || tiles > 4 || p.T < 2 * near) return c;
+  c.tiles = std::min(tiles, ntiles);
+  c.parts = (int)std::min<int64_t>(64, p.T / near);
+  return c;
+}
+
+size_t cut_bytes(const AttnParams& p, const Cut& c) {
+  return c.tiles ? (size_t)p.B * p.Hkv * c.tiles * c.parts * kBA * 2 * p.D * sizeof(float) : 0;
+}
+
 template <typename T, int DP>
-cudaError_t backward_dp(const AttnParams& p, cudaStream_t stream) {
+cudaError_t backward_dp(const AttnParams& p, float* part, cudaStream_t stream) {
   constexpr int BB = 32;
   constexpr int bytes = ((2 * kBA + 2 * BB) * (DP + 4) + 2 * kBA * (BB + 4) + 2 * kBA) * 4;
   static_assert(bytes <= 232448, "shared memory budget");
+  Cut cut = cut_for(p);
+  cut.part = part;
   if (p.dk || p.dv) {
     cudaError_t e = set_smem_limit<attn_simt_backward_kernel<T, DP, false>>(bytes);
     if (e != cudaSuccess) return e;
     const int nt = (p.T + kBA - 1) / kBA;
-    const int64_t grid = (int64_t)nt * p.Hkv * p.B;
+    const int64_t pairs = (int64_t)p.Hkv * p.B;
+    const int64_t grid = (nt + (int64_t)cut.tiles * (cut.parts - 1)) * pairs;
     if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    attn_simt_backward_kernel<T, DP, false><<<(unsigned)grid, kThreads, bytes, stream>>>(p, nt);
+    attn_simt_backward_kernel<T, DP, false><<<(unsigned)grid, kThreads, bytes, stream>>>(p, nt, cut);
     e = cudaGetLastError();
+    if (e == cudaSuccess && cut.tiles) {
+      const int64_t n = pairs * cut.tiles * kBA * (p.D / 2);
+      cut_sum_kernel<T><<<(unsigned)((n + 255) / 256), 256, 0, stream>>>(p, cut);
+      e = cudaGetLastError();
+    }
     if (e != cudaSuccess) return e;
   }
   if (p.dq) {
@@ -468,7 +560,7 @@ cudaError_t backward_dp(const AttnParams& p, cudaStream_t stream) {
     const int64_t nt = row_tiles(p);
     const int64_t grid = nt * p.Hkv * p.B;
     if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    attn_simt_backward_kernel<T, DP, true><<<(unsigned)grid, kThreads, bytes, stream>>>(p, (int)nt);
+    attn_simt_backward_kernel<T, DP, true><<<(unsigned)grid, kThreads, bytes, stream>>>(p, (int)nt, cut);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
@@ -485,13 +577,15 @@ cudaError_t launch_attn_simt(const AttnParams& p, rsm_dtype dtype, cudaStream_t 
                    : p.D <= 128 ? forward_dp<__nv_bfloat16, 128>(p, stream) : forward_dp<__nv_bfloat16, 256>(p, stream);
 }
 
-cudaError_t launch_attn_simt_backward(const AttnParams& p, rsm_dtype dtype, cudaStream_t stream) {
+size_t attn_simt_backward_bytes(const AttnParams& p) { return cut_bytes(p, cut_for(p)); }
+
+cudaError_t launch_attn_simt_backward(const AttnParams& p, rsm_dtype dtype, float* part, cudaStream_t stream) {
   if (dtype == RSM_F32)
-    return p.D <= 64 ? backward_dp<float, 64>(p, stream)
-                     : p.D <= 128 ? backward_dp<float, 128>(p, stream) : backward_dp<float, 256>(p, stream);
-  return p.D <= 64 ? backward_dp<__nv_bfloat16, 64>(p, stream)
-                   : p.D <= 128 ? backward_dp<__nv_bfloat16, 128>(p, stream)
-                                : backward_dp<__nv_bfloat16, 256>(p, stream);
+    return p.D <= 64 ? backward_dp<float, 64>(p, part, stream)
+                     : p.D <= 128 ? backward_dp<float, 128>(p, part, stream) : backward_dp<float, 256>(p, part, stream);
+  return p.D <= 64 ? backward_dp<__nv_bfloat16, 64>(p, part, stream)
+                   : p.D <= 128 ? backward_dp<__nv_bfloat16, 128>(p, part, stream)
+                                : backward_dp<__nv_bfloat16, 256>(p, part, stream);
 }
 
 cudaError_t launch_attn_delta(const AttnParams& p, rsm_dtype dtype, cudaStream_t stream) {

@@ -119,7 +119,8 @@ size_t delta_bytes(const rsm_window_backward_args& a) { return up256((size_t)a.B
 
 size_t window_backward_bytes(const rsm_window_backward_args& a) {
   const rsm::AttnParams p = window_params(a);
-  return rsm::attn_tc_supported(p, a.dtype) ? rsm::attn_tc_backward_bytes(p) : delta_bytes(a);
+  return rsm::attn_tc_supported(p, a.dtype) ? rsm::attn_tc_backward_bytes(p)
+                                             : delta_bytes(a) + rsm::attn_simt_backward_bytes(p);
 }
 
 rsm_status check_cache(int B, int N, int Hkv, int D, int num_pages, int page_size, int table_width) {
@@ -251,7 +252,7 @@ rsm_status rsm_window_backward(const rsm_window_backward_args* a, void* stream) 
   } else if (e == cudaSuccess) {
     p.delta = static_cast<float*>(a->workspace);
     e = rsm::launch_attn_delta(p, a->dtype, st);
-    if (e == cudaSuccess) e = rsm::launch_attn_simt_backward(p, a->dtype, st);
+    if (e == cudaSuccess) e = rsm::launch_attn_simt_backward(p, a->dtype, reinterpret_cast<float*>(static_cast<char*>(a->workspace) + delta_bytes(*a)), st);
   }
   return finish(e, "rsm_window_backward");
 }

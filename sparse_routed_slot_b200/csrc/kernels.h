@@ -73,7 +73,8 @@ struct AttnParams {
 // CUDA-core kernels in fp32 (any dtype, head dimension and page size).
 int attn_simt_splits(const AttnParams& p);
 cudaError_t launch_attn_simt(const AttnParams& p, rsm_dtype dtype, cudaStream_t stream);
-cudaError_t launch_attn_simt_backward(const AttnParams& p, rsm_dtype dtype, cudaStream_t stream);
+size_t attn_simt_backward_bytes(const AttnParams& p);  // of `part`
+cudaError_t launch_attn_simt_backward(const AttnParams& p, rsm_dtype dtype, float* part, cudaStream_t stream);
 // Tensor-core forward (attn_tc.cu): bf16, head dimensions to 128, page sizes that fit its tiles.
 bool attn_tc_supported(const AttnParams& p, rsm_dtype dtype);
 int attn_tc_splits(const AttnParams& p);

@@ -11,8 +11,11 @@
 //
 // All products have the same two shapes, 64 stationary rows (16 x 16 threads, 4 rows each) against
 // BB streamed ones: W = A B^T over the head dimension and acc += W B. Both read 16-byte pieces of
-// shared memory, the rows padded by 16 bytes so that 8 neighbouring rows use different banks; 8 FMAs
-// per load instruction keep the FMA pipe, not shared memory, the bound.
+// shared memory, the rows padded by 16 bytes so that 8 neighbouring rows use different banks. What bounds
+// them is shared memory, which hands out 32 words a cycle: a thread's 4 x 4 (4 x 2) products use a word
+// twice (1.3 times) and the FMA pipe could take 4. Neither 8 rows per thread and half the threads (window
+// train fp32 234 us against 180) nor warp-level tf32 products of split operands (201 us) were faster at
+// the sizes fp32 runs at, where blocks are few and latency counts.
 #include <algorithm>
 
 #include "attention.cuh"
@@ -48,8 +51,15 @@ template <> struct Out<__nv_bfloat16> {
 // offset(r) < 0. 16 threads share a row, so a row's offset (divisions by the group or page size) is found
 // once per 16 bytes x D / 64 and thread. Columns past D are left alone: no product reads them into a
 // column that is stored. With `used`, it gets whether each row is there.
+RSM_DEV float4 read4(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
+RSM_DEV float4 read4(const __nv_bfloat16* p) {
+  const uint2 t = __ldg(reinterpret_cast<const uint2*>(p));
+  return make_float4(__uint_as_float(t.x << 16), __uint_as_float(t.x & 0xffff0000u), __uint_as_float(t.y << 16),
+                     __uint_as_float(t.y & 0xffff0000u));
+}
 template <typename T, int DP, int N, class Off>
 RSM_DEV void load_rows(float* dst, const void* base, int D, int tx, int ty, Off offset, int* used = nullptr) {
+  float4 x[N / 16][DP / 64];  // (all loads before the first store: one trip to memory, not one per row)
 #pragma unroll
   for (int k = 0; k < N / 16; ++k) {
     const int r = ty + 16 * k;
@@ -58,12 +68,16 @@ RSM_DEV void load_rows(float* dst, const void* base, int D, int tx, int ty, Off 
 #pragma unroll
     for (int jj = 0; jj < DP / 64; ++jj) {
       const int c = 4 * tx + 64 * jj;
-      if (c >= D) continue;
-      float x[4] = {0.f, 0.f, 0.f, 0.f};
-      if (off >= 0) In<T>::ld4(static_cast<const T*>(base) + off + c, x);
-      *reinterpret_cast<float4*>(dst + r * (DP + 4) + c) = make_float4(x[0], x[1], x[2], x[3]);
+      x[k][jj] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (off >= 0 && c < D) x[k][jj] = read4(static_cast<const T*>(base) + off + c);
     }
   }
+#pragma unroll
+  for (int k = 0; k < N / 16; ++k)
+#pragma unroll
+    for (int jj = 0; jj < DP / 64; ++jj)
+      if (4 * tx + 64 * jj < D)
+        *reinterpret_cast<float4*>(dst + (ty + 16 * k) * (DP + 4) + 4 * tx + 64 * jj) = x[k][jj];
 }
 
 // c[i][j] = sum_d A[ty + 16 i][d] B[tx + 16 j][d]
@@ -514,16 +528,24 @@ cudaError_t forward_dp(const AttnParams& p, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
-// Tiles whose keys are all behind the sinks are left whole; so is everything where the walk past the window
-// is no longer than the window, or where there are so many sinks that the walks are all alike.
+// The tiles that hold sinks are cut where the walk past the window is longer than the window (unless there
+// are so many that the walks are all alike). All tiles are, where whole ones would leave SMs idle.
 Cut cut_for(const AttnParams& p) {
   Cut c{0, 1, nullptr};
   const int ntiles = (p.T + kBA - 1) / kBA;
   const int tiles = (std::min(p.sinks, p.T) + kBA - 1) / kBA;
   const int64_t near = std::min<int64_t>(p.T, (int64_t)kBA + p.window);
-  if (tiles == 0 || tiles > 4 || p.T < 2 * near) return c;
-  c.tiles = std::min(tiles, ntiles);
-  c.parts = (int)std::min<int64_t>(64, p.T / near);
+  if (tiles > 0 && tiles <= 4 && p.T >= 2 * near) {
+    c.tiles = std::min(tiles, ntiles);
+    c.parts = (int)std::min<int64_t>(64, p.T / near);
+  }
+  const int64_t blocks = std::max<int64_t>(1, (int64_t)ntiles * p.Hkv * p.B);
+  const int64_t steps = near * p.G / 32;  // of a whole tile
+  const int parts = (int)std::min<int64_t>({device_sm_count() / blocks, steps / 2, 8});
+  if (parts > 1) {
+    c.tiles = ntiles;
+    c.parts = std::max(c.parts, parts);
+  }
   return c;
 }
 

@@ -88,9 +88,16 @@ template <class A> rsm::AttnParams window_params(const A& a) {
   return p;
 }
 
-// bf16 of head dimensions to 128 runs on the tensor cores, everything else in fp32 on CUDA cores.
+// bf16: up to 16 query rows per key/value head and sequence are bound by the cache's read and take the
+// register kernel, else head dimensions to 128 run on the tensor cores in tiles. Everything else runs in fp32
+// on CUDA cores.
 cudaError_t launch_forward(const rsm::AttnParams& p, rsm_dtype dtype, cudaStream_t st) {
+  if (rsm::attn_decode_supported(p, dtype)) return rsm::launch_attn_decode(p, st);
   return rsm::attn_tc_supported(p, dtype) ? rsm::launch_attn_tc(p, st) : rsm::launch_attn_simt(p, dtype, st);
+}
+int forward_splits(const rsm::AttnParams& p, rsm_dtype dtype) {
+  if (rsm::attn_decode_supported(p, dtype)) return rsm::attn_decode_splits(p);
+  return rsm::attn_tc_supported(p, dtype) ? rsm::attn_tc_splits(p) : rsm::attn_simt_splits(p);
 }
 
 template <class A> cudaError_t validate_qkv(const A& a, cudaStream_t st) {
@@ -162,7 +169,7 @@ rsm::AttnParams paged_params(const rsm_paged_args& a) {
   p.cu_q = a.cu_q; p.kv_len = a.kv_len;
   p.num_pages = a.num_pages; p.page = a.page_size; p.table_width = a.table_width;
   p.max_q = std::min(a.max_q, a.N);
-  p.splits = rsm::attn_tc_supported(p, a.dtype) ? rsm::attn_tc_splits(p) : rsm::attn_simt_splits(p);
+  p.splits = forward_splits(p, a.dtype);
   return p;
 }
 

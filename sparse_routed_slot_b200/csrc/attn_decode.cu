@@ -1,10 +1,12 @@
 // attn_decode.cu -- paged attention of single tokens (and other calls with at most 16 query rows per
 // key/value head and sequence), bf16.
 //
-// Such a call reads every key and value once and computes little: it is bound by that read. K and V go
-// straight from memory to registers, 16 bytes per lane, in the layout that the warp-level tensor products
-// (m16n8k16) want, so there is no shared memory, no barrier and nothing to wait for but the data. With Q's
-// rows as the narrow side of the products no row of them is wasted on up to 8 query rows:
+// Such a call reads every key and value once and computes little: it is bound by that read. Each warp walks
+// its own tiles of 16 keys (every eighth of the block's) through a ring in shared memory that it fills by
+// asynchronous copies, 16 bytes per lane, two tiles ahead: 8 warps keep 128 KB in flight (head dimension 128),
+// and no warp waits for another until the end. (Straight to registers, 16 warps with a tile each got 4.0 TB/s,
+// 8 warps with two tiles 3.7.) The rest are warp-level tensor products (m16n8k16) with Q's rows as the narrow
+// side, so that none of it is wasted on up to 8 query rows:
 //   S^T = K Q^T   16 keys x 8 rows. A product sums over columns in any order, so lane 4 g + t takes the
 //                 contiguous columns 8 t .. 8 t + 7 of a block of 32 for keys g and g + 8
 //   O^T += V^T P^T  16 columns x 8 rows over 16 keys. The lane has columns 8 g .. 8 g + 7 of keys 2 t, 2 t + 1,
@@ -12,11 +14,8 @@
 //                 8 g + 2 j (+ 1) stands in row g (g + 8) of product j
 //   P^T from S^T's accumulators by an 8 x 8 transpose across the lanes.
 // The weights are rounded to bf16 for the product; scores, statistics and sums are fp32. As in the tile
-// kernel, the reference of a row's exponentials moves only past 2^32.
-//
-// Each warp walks its own tiles of 16 keys (every eighth of the block's) and the block's warps join at the
-// end in shared memory, blocks that share a sequence's keys in a second kernel. 16 warps per SM keep
-// 16 x 8 KB on their way (head dimension 128); the copy's rate needs about 45 KB.
+// kernel, the reference of a row's exponentials moves only past 2^32. The block's warps join at the end in
+// shared memory, blocks that share a sequence's keys in a second kernel.
 #include <algorithm>
 
 #include "attention.cuh"
@@ -27,7 +26,6 @@ namespace {
 
 using namespace attn;
 
-constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr int kKeys = 16;
 constexpr float kNegInf = -__builtin_inff();
 constexpr float kSlack = 32.f;
@@ -64,12 +62,33 @@ RSM_DEV float over_keys_sum(float v) {
   return v;
 }
 
+template <int DP> struct Layout {
+  static constexpr int kWarps = DP <= 128 ? 8 : 4, kThreads = 32 * kWarps;
+  static constexpr int kTile = kKeys * DP * 2;            // bytes of a tile of keys (or values)
+  static constexpr int kStages = DP <= 64 ? 6 : 3;        // 192 KB in all
+  static constexpr int kBytes = kWarps * kStages * 2 * kTile;
+};
+
+// 16 bytes to shared memory, or zeros.
+RSM_DEV void copy16(uint32_t to, const void* from, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(there ? 16 : 0) : "memory");
+}
+RSM_DEV uint4 lds16(uint32_t at) {
+  uint4 x;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(at));
+  return x;
+}
+
 // NQ: groups of 8 query rows. A row is (token, head of the group), as everywhere.
 template <int DP, int NQ>
-__global__ void __launch_bounds__(kThreads, DP <= 128 && NQ == 1 ? 2 : 1) attn_decode_kernel(const AttnParams p) {
+__global__ void __launch_bounds__(Layout<DP>::kThreads, 1) attn_decode_kernel(const AttnParams p) {
+  using L = Layout<DP>;
+  constexpr int kWarps = L::kWarps, kThreads = L::kThreads, kStages = L::kStages;
   constexpr int kR = 8 * NQ;
   constexpr int kC = DP / 32, kB = DP / 64;  // blocks of columns of the two products
-  extern __shared__ float sm[];              // [warps][kR][DP]
+  constexpr int kPieces = DP / 8;            // 16-byte pieces of a row
+  extern __shared__ float sm[];              // the warps' rings, and at the end [warps][kR][DP]
+  static_assert(kWarps * kR * DP * 4 <= L::kBytes, "the results fit the rings");
   __shared__ float s_m[kWarps][kR], s_l[kWarps][kR];
   const int split = blockIdx.x % p.splits;
   const int pair = blockIdx.x / p.splits;
@@ -101,9 +120,12 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 && NQ == 1 ? 2 : 1) attn_d
   const int64_t row_step = (int64_t)p.Hkv * D;
   const bool one_page = p.page % kKeys == 0;  // a tile of keys stands in one page
   float m[NQ][2], l[NQ][2], o[NQ][kB * 4][4];
+  int pos[NQ][2];  // places of rows 8 n + 2 t and + 1
 #pragma unroll
   for (int n = 0; n < NQ; ++n) {
     m[n][0] = m[n][1] = kNegInf;
+    pos[n][0] = s.pos0 + (8 * n + 2 * t) / G;
+    pos[n][1] = s.pos0 + (8 * n + 2 * t + 1) / G;
     l[n][0] = l[n][1] = 0.f;
 #pragma unroll
     for (int j = 0; j < kB * 4; ++j) o[n][j][0] = o[n][j][1] = o[n][j][2] = o[n][j][3] = 0.f;
@@ -116,34 +138,56 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 && NQ == 1 ? 2 : 1) attn_d
   auto tile_base = [&](int w) -> int64_t {
     return one_page && w < w1 ? kv_offset(p, b, hk, walk.tile(w) * kKeys) : -1;
   };
-  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-  int64_t base = tile_base(w0 + warp);
-#pragma unroll 1
-  for (int w = w0 + warp; w < w1; w += kWarps) {
+  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(sm) + warp * (kStages * 2 * L::kTile);
+  // Pieces stand in an order of their own per row, so that the 8 lanes of a quarter warp read different banks:
+  // lanes g = 2 i, 2 i + 1 and all t of the keys, lanes g = 2 i, 2 i + 1 and rows 2 t of the values.
+  auto k_at = [](int row, int piece) { return (uint32_t)(row * DP * 2 + ((piece ^ ((row & 1) << 2)) << 4)); };
+  auto v_at = [](int row, int piece) { return (uint32_t)(row * DP * 2 + ((piece ^ (row & 6)) << 4)); };
+  // Nearly every tile is a whole one of one page: its addresses are a lane's place plus multiples of a row, its
+  // scores are all seen. (With the general arithmetic for every tile, 780 instructions per tile and warp, the
+  // arithmetic and not the memory set the pace: 434 us for the step of 256.)
+  const bool full_rows = one_page && D == DP;
+  const __nv_bfloat16* lane_k = static_cast<const __nv_bfloat16*>(p.k) + (lane / kPieces) * row_step + 8 * (lane % kPieces);
+  const __nv_bfloat16* lane_v = static_cast<const __nv_bfloat16*>(p.v) + (lane / kPieces) * row_step + 8 * (lane % kPieces);
+  const int64_t hop = (32 / kPieces) * row_step;  // from one copy of the lane to its next
+  auto fetch = [&](int w, int64_t base, int stage) {
+    const uint32_t to = ring + stage * 2 * L::kTile;
     const int k0 = walk.tile(w) * kKeys;
-    uint4 k[2][kC], v[4][kB];
-    int64_t ko[2];
+    if (full_rows && w < w1 && base >= 0 && k0 + kKeys <= s.kv) {
+      const __nv_bfloat16 *fk = lane_k + base, *fv = lane_v + base;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      ko[i] = offset(k0, g + 8 * i, base);
-#pragma unroll
-      for (int c = 0; c < kC; ++c) {
-        const int d = 32 * c + 8 * t;
-        k[i][c] = zero;
-        if (ko[i] >= 0 && d < D) k[i][c] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.k) + ko[i] + d));
+      for (int i = 0; i < kKeys * kPieces / 32; ++i) {
+        const int row = 32 / kPieces * i + lane / kPieces;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + k_at(row, lane % kPieces)), "l"(fk) : "memory");
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + L::kTile + v_at(row, lane % kPieces)), "l"(fv)
+                     : "memory");
+        fk += hop;
+        fv += hop;
       }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      return;
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t vo = offset(k0, 2 * t + (i & 1) + 8 * (i >> 1), base);
-#pragma unroll
-      for (int c = 0; c < kB; ++c) {
-        const int d = 64 * c + 8 * g;
-        v[i][c] = zero;
-        if (vo >= 0 && d < D) v[i][c] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.v) + vo + d));
-      }
+    for (int i = 0; i < kKeys * kPieces / 32; ++i) {
+      const int row = (32 * i + lane) / kPieces, piece = lane % kPieces;
+      const int64_t off = w < w1 ? offset(k0, row, base) : -1;
+      const bool there = off >= 0 && 8 * piece < D;
+      const int64_t at = there ? off + 8 * piece : 0;
+      copy16(to + k_at(row, piece), static_cast<const __nv_bfloat16*>(p.k) + at, there);
+      copy16(to + L::kTile + v_at(row, piece), static_cast<const __nv_bfloat16*>(p.v) + at, there);
     }
-    base = tile_base(w + kWarps);  // the table's answer for the next tile comes meanwhile
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  auto attend = [&](int w, int64_t base, int stage) {
+    const int k0 = walk.tile(w) * kKeys;
+    const uint32_t from = ring + stage * 2 * L::kTile;
+    const bool whole = one_page && base >= 0 && k0 + kKeys <= s.kv && k0 + kKeys - 1 <= s.pos0 &&
+                       (p.window <= 0 || s.pos0 + nq - 1 - k0 < p.window || k0 + kKeys <= p.sinks);
+    uint4 k[2][kC];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int c = 0; c < kC; ++c) k[i][c] = lds16(from + k_at(g + 8 * i, 4 * c + t));
     uint32_t pt[NQ][2];            // the weights as the second product takes them
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
@@ -153,12 +197,15 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 && NQ == 1 ? 2 : 1) attn_d
         mma(c4, k[0][c].x, k[1][c].x, k[0][c].y, k[1][c].y, q[n][c].x, q[n][c].y);
         mma(c4, k[0][c].z, k[1][c].z, k[0][c].w, k[1][c].w, q[n][c].z, q[n][c].w);
       }
-      // c4[e]: key g + 8 (e / 2), row 2 t + e % 2
+      // c4[e]: key g + 8 (e / 2), row 2 t + e % 2 (rows past the last are zeros, and stay finite)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int key = k0 + g + 8 * (e >> 1), r = 8 * n + 2 * t + (e & 1);
-        const bool seen = ko[e >> 1] >= 0 && r < rows && sees(s.pos0 + r / G, key, p.window, p.sinks);
-        c4[e] = seen ? c4[e] * scale2 : kNegInf;
+      for (int e = 0; e < 4; ++e) c4[e] *= scale2;
+      if (!whole) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int i = g + 8 * (e >> 1);
+          if (offset(k0, i, base) < 0 || !sees(pos[n][e & 1], k0 + i, p.window, p.sinks)) c4[e] = kNegInf;
+        }
       }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
@@ -184,18 +231,44 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 && NQ == 1 ? 2 : 1) attn_d
     }
 #pragma unroll
     for (int c = 0; c < kB; ++c) {
-      const uint32_t x[4][4] = {{v[0][c].x, v[0][c].y, v[0][c].z, v[0][c].w},
-                                {v[1][c].x, v[1][c].y, v[1][c].z, v[1][c].w},
-                                {v[2][c].x, v[2][c].y, v[2][c].z, v[2][c].w},
-                                {v[3][c].x, v[3][c].y, v[3][c].z, v[3][c].w}};
+      uint32_t v[4][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint4 x = lds16(from + L::kTile + v_at(2 * t + (i & 1) + 8 * (i >> 1), 8 * c + g));
+        v[i][0] = x.x; v[i][1] = x.y; v[i][2] = x.z; v[i][3] = x.w;
+      }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const uint32_t a0 = __byte_perm(x[0][j], x[1][j], 0x5410), a1 = __byte_perm(x[0][j], x[1][j], 0x7632);
-        const uint32_t a2 = __byte_perm(x[2][j], x[3][j], 0x5410), a3 = __byte_perm(x[2][j], x[3][j], 0x7632);
+        const uint32_t a0 = __byte_perm(v[0][j], v[1][j], 0x5410), a1 = __byte_perm(v[0][j], v[1][j], 0x7632);
+        const uint32_t a2 = __byte_perm(v[2][j], v[3][j], 0x5410), a3 = __byte_perm(v[2][j], v[3][j], 0x7632);
 #pragma unroll
         for (int n = 0; n < NQ; ++n) mma(o[n][4 * c + j], a0, a1, a2, a3, pt[n][0], pt[n][1]);
       }
     }
+  };
+  {
+    // `base` of the tiles in the ring and of the one after them: the table's answer comes a step ahead of its use
+    int64_t bases[kStages];
+#pragma unroll
+    for (int i = 0; i < kStages; ++i) bases[i] = tile_base(w0 + warp + i * kWarps);
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) fetch(w0 + warp + i * kWarps, bases[i], i);
+    int stage = 0;
+#pragma unroll 1
+    for (int w = w0 + warp; w < w1; w += kWarps) {
+      fetch(w + (kStages - 1) * kWarps, bases[kStages - 1], stage == 0 ? kStages - 1 : stage - 1);
+      const int64_t coming = tile_base(w + kStages * kWarps);
+      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+      __syncwarp();  // every lane's part of the tile
+      attend(w, bases[0], stage);
+      __syncwarp();  // the stage may be filled again
+#pragma unroll
+      for (int i = 0; i + 1 < kStages; ++i) bases[i] = bases[i + 1];
+      bases[kStages - 1] = coming;
+      stage = stage + 1 == kStages ? 0 : stage + 1;
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();
   }
   // ---- the warps' results. o[n][4 c + j][e]: column 64 c + 8 g + 2 j + e / 2, row 8 n + 2 t + e % 2
 #pragma unroll
@@ -248,12 +321,13 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 && NQ == 1 ? 2 : 1) attn_d
 }
 
 template <int DP, int NQ> cudaError_t launch_as(const AttnParams& p, cudaStream_t stream) {
-  constexpr int bytes = kWarps * 8 * NQ * DP * 4;
+  constexpr int bytes = Layout<DP>::kBytes;
+  static_assert(bytes <= 232448 - 4096, "shared memory budget");
   cudaError_t e = set_smem_limit<attn_decode_kernel<DP, NQ>>(bytes);
   if (e != cudaSuccess) return e;
   const int64_t grid = (int64_t)p.B * p.Hkv * p.splits;
   if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  attn_decode_kernel<DP, NQ><<<(unsigned)grid, kThreads, bytes, stream>>>(p);
+  attn_decode_kernel<DP, NQ><<<(unsigned)grid, Layout<DP>::kThreads, bytes, stream>>>(p);
   return cudaGetLastError();
 }
 
@@ -269,7 +343,7 @@ int attn_decode_splits(const AttnParams& p) {
   int64_t keys = (int64_t)p.table_width * p.page;
   if (p.window > 0) keys = std::min<int64_t>(keys, (int64_t)p.window + p.sinks + p.max_q);
   const int64_t want = 4 * device_sm_count() / std::max<int64_t>(1, (int64_t)p.B * p.Hkv);
-  return (int)std::max<int64_t>(1, std::min<int64_t>({want, keys / (kKeys * kWarps), 64}));
+  return (int)std::max<int64_t>(1, std::min<int64_t>({want, keys / (kKeys * 8), 64}));
 }
 
 cudaError_t launch_attn_decode(const AttnParams& p, cudaStream_t stream) {

@@ -15,7 +15,11 @@
 //   P^T from S^T's accumulators by an 8 x 8 transpose across the lanes.
 // The weights are rounded to bf16 for the product; scores, statistics and sums are fp32. As in the tile
 // kernel, the reference of a row's exponentials moves only past 2^32. The block's warps join at the end in
-// shared memory, blocks that share a sequence's keys in a second kernel.
+// shared memory. Up to 8 blocks that share a sequence's keys are a cluster and join through each other's
+// shared memory (one launch and no workspace: the step of one short sequence 31 -> 24 us a call); more leave
+// their results to a second kernel.
+#include <cooperative_groups.h>
+
 #include <algorithm>
 
 #include "attention.cuh"
@@ -29,6 +33,7 @@ using namespace attn;
 constexpr int kKeys = 16;
 constexpr float kNegInf = -__builtin_inff();
 constexpr float kSlack = 32.f;
+constexpr int kCluster = 8;  // blocks that may join through shared memory
 
 RSM_DEV void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -88,8 +93,8 @@ __global__ void __launch_bounds__(Layout<DP>::kThreads, 1) attn_decode_kernel(co
   constexpr int kC = DP / 32, kB = DP / 64;  // blocks of columns of the two products
   constexpr int kPieces = DP / 8;            // 16-byte pieces of a row
   extern __shared__ float sm[];              // the warps' rings, and at the end [warps][kR][DP]
-  static_assert(kWarps * kR * DP * 4 <= L::kBytes, "the results fit the rings");
-  __shared__ float s_m[kWarps][kR], s_l[kWarps][kR];
+  static_assert((kWarps + 1) * kR * DP * 4 <= L::kBytes, "the results fit the rings");
+  __shared__ float s_m[kWarps][kR], s_l[kWarps][kR], s_top[kR], s_sum[kR];
   const int split = blockIdx.x % p.splits;
   const int pair = blockIdx.x / p.splits;
   const int hk = pair % p.Hkv, b = pair / p.Hkv;
@@ -290,6 +295,21 @@ __global__ void __launch_bounds__(Layout<DP>::kThreads, 1) attn_decode_kernel(co
     }
   __syncthreads();
   const int64_t total = (int64_t)p.T * p.H;
+  const bool joined = p.splits > 1 && p.splits <= kCluster;
+  float* mine = sm + kWarps * kR * DP;  // the block's own sums, where the cluster reads them: [kR][DP]
+  auto finish = [&](int r, int d, float4 a, float sum, float ref) {
+    const float inv = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;  // (a NaN stays one)
+    const int64_t at = q_index(r);
+    const float lse = sum == 0.f ? kNegInf : (ref + log2f(sum)) * kLn2;
+    a = make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
+    if (p.splits > kCluster) {
+      *reinterpret_cast<float4*>(p.part_o + (split * total + at) * D + d) = a;
+      if (d == 0) p.part_lse[split * total + at] = lse;
+    } else {
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + at * D + d) = make_uint2(pack(a.x, a.y), pack(a.z, a.w));
+      if (d == 0 && p.lse) p.lse[at] = lse;
+    }
+  };
   for (int e = threadIdx.x; e < rows * (D / 4); e += kThreads) {
     const int r = e / (D / 4), d = (e - r * (D / 4)) * 4;
     float top = kNegInf;
@@ -305,19 +325,36 @@ __global__ void __launch_bounds__(Layout<DP>::kThreads, 1) attn_decode_kernel(co
       sum = fmaf(f, s_l[w][r], sum);
       a.x = fmaf(f, x.x, a.x); a.y = fmaf(f, x.y, a.y); a.z = fmaf(f, x.z, a.z); a.w = fmaf(f, x.w, a.w);
     }
-    const float inv = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;  // (a NaN stays one)
-    const int64_t at = q_index(r);
-    if (p.splits > 1)
-      *reinterpret_cast<float4*>(p.part_o + (split * total + at) * D + d) = make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
-    else
-      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + at * D + d) =
-          make_uint2(pack(a.x * inv, a.y * inv), pack(a.z * inv, a.w * inv));
-    if (d == 0) {
-      const float lse = sum == 0.f ? kNegInf : (ref + log2f(sum)) * kLn2;
-      if (p.splits > 1) p.part_lse[split * total + at] = lse;
-      else if (p.lse) p.lse[at] = lse;
+    if (!joined) {
+      finish(r, d, a, sum, ref);
+    } else {
+      *reinterpret_cast<float4*>(mine + r * DP + d) = a;
+      if (d == 0) {
+        s_top[r] = top;
+        s_sum[r] = sum;
+      }
     }
   }
+  if (!joined) return;
+  // every block of the cluster has its sums ready; each finishes its share of the outputs
+  cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
+  cluster.sync();
+  for (int e = split * kThreads + threadIdx.x; e < rows * (D / 4); e += p.splits * kThreads) {
+    const int r = e / (D / 4), d = (e - r * (D / 4)) * 4;
+    float top = kNegInf;
+    for (int i = 0; i < p.splits; ++i) top = fmaxf(top, *cluster.map_shared_rank(&s_top[r], i));
+    const float ref = top == kNegInf ? 0.f : top;
+    float sum = 0.f;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < p.splits; ++i) {
+      const float f = ex2(*cluster.map_shared_rank(&s_top[r], i) - ref);
+      const float4 x = *reinterpret_cast<const float4*>(cluster.map_shared_rank(mine + r * DP + d, i));
+      sum = fmaf(f, *cluster.map_shared_rank(&s_sum[r], i), sum);
+      a.x = fmaf(f, x.x, a.x); a.y = fmaf(f, x.y, a.y); a.z = fmaf(f, x.z, a.z); a.w = fmaf(f, x.w, a.w);
+    }
+    finish(r, d, a, sum, ref);
+  }
+  cluster.sync();  // no block leaves while another reads its memory
 }
 
 template <int DP, int NQ> cudaError_t launch_as(const AttnParams& p, cudaStream_t stream) {
@@ -327,8 +364,22 @@ template <int DP, int NQ> cudaError_t launch_as(const AttnParams& p, cudaStream_
   if (e != cudaSuccess) return e;
   const int64_t grid = (int64_t)p.B * p.Hkv * p.splits;
   if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  attn_decode_kernel<DP, NQ><<<(unsigned)grid, Layout<DP>::kThreads, bytes, stream>>>(p);
-  return cudaGetLastError();
+  if (p.splits == 1 || p.splits > kCluster) {
+    attn_decode_kernel<DP, NQ><<<(unsigned)grid, Layout<DP>::kThreads, bytes, stream>>>(p);
+    return cudaGetLastError();
+  }
+  cudaLaunchConfig_t config = {};
+  config.gridDim = dim3((unsigned)grid);
+  config.blockDim = dim3(Layout<DP>::kThreads);
+  config.dynamicSmemBytes = bytes;
+  config.stream = stream;
+  cudaLaunchAttribute cluster;
+  cluster.id = cudaLaunchAttributeClusterDimension;
+  cluster.val.clusterDim.x = (unsigned)p.splits;
+  cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
+  config.attrs = &cluster;
+  config.numAttrs = 1;
+  return cudaLaunchKernelEx(&config, attn_decode_kernel<DP, NQ>, p);
 }
 
 }  // namespace
@@ -345,6 +396,8 @@ int attn_decode_splits(const AttnParams& p) {
   const int64_t want = 4 * device_sm_count() / std::max<int64_t>(1, (int64_t)p.B * p.Hkv);
   return (int)std::max<int64_t>(1, std::min<int64_t>({want, keys / (kKeys * 8), 64}));
 }
+
+bool attn_decode_joins(const AttnParams& p) { return p.splits <= kCluster; }
 
 cudaError_t launch_attn_decode(const AttnParams& p, cudaStream_t stream) {
   const bool two = p.max_q * p.G > 8;

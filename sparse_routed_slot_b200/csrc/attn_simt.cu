@@ -544,7 +544,7 @@ Cut cut_for(const AttnParams& p) {
   const int parts = (int)std::min<int64_t>({device_sm_count() / blocks, steps / 2, 8});
   if (parts > 1) {
     c.tiles = ntiles;
-    c.parts = std::max(c.parts, parts);
+    c.parts = std::max(std::min(c.parts, 8), parts);
   }
   return c;
 }

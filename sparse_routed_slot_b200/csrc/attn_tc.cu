@@ -61,10 +61,9 @@ template <int DP> struct Layout {
 struct Steps {
   int sinks, first, end;
   RSM_DEV bool operator()(int i) const { return i < end && (i >= first || i < sinks); }
-  RSM_DEV int count(int n) const {
-    int c = 0;
-    for (int i = 0; i < n; ++i) c += (*this)(i);
-    return c;
+  RSM_DEV int count() const {
+    const int a = max(0, min(sinks, end));
+    return a + max(0, end - max(a, first));
   }
 };
 
@@ -267,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     // The warps of both tiles that share a scheduler form their weights in turn: see above.
     const Steps other = steps_of(walk, w0, n, pos0 + (1 - t) * tok_tile, pos0 + (1 - t) * tok_tile + (t ? ntok0 : ntok1) - 1,
                                  s.kv, p, t || ntiles > 1);
-    const int theirs = other.count(n);
+    const int theirs = other.count();
     const int my_turn = 1 + 2 * (warp & 3) + t, their_turn = 1 + 2 * (warp & 3) + 1 - t;
     int last = 0;  // the step before this one
     // Scores of step i into x (hidden ones -inf), and the row's reference moved where it has to. False: a wait expired.

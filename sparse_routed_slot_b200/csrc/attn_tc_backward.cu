@@ -418,14 +418,12 @@ __global__ void __launch_bounds__(256) stat_kernel(const AttnParams p, int64_t r
 }
 
 // Adds the chunks of the sink rows up, in order, a warp per row.
-__global__ void __launch_bounds__(256) sink_sum_kernel(const AttnParams p, Chunks ch) {
+__global__ void __launch_bounds__(256) sink_sum_kernel(const AttnParams p, Chunks ch, int sinks) {
   const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
-  const int r = (int)(w % kBM);
-  const int kt = (int)(w / kBM % ch.sink_tiles);
-  const int64_t pair = w / kBM / ch.sink_tiles;
-  const int key = kt * kBM + r;
-  if (pair >= (int64_t)p.B * p.Hkv || key >= p.sinks || key >= p.T) return;
+  const int key = (int)(w % sinks), kt = key / kBM, r = key % kBM;
+  const int64_t pair = w / sinks;
+  if (pair >= (int64_t)p.B * p.Hkv) return;
   const int hk = (int)(pair % p.Hkv);
   const int64_t b = pair / p.Hkv;
   const float* part = ch.part + ((pair * ch.sink_tiles + kt) * (ch.far + 1) * kBM + r) * 2 * p.D;
@@ -489,7 +487,8 @@ cudaError_t launch_run(const Maps& maps, const AttnParams& p, const Chunks& ch, 
   attn_tc_backward_kernel<DP, DQ><<<(unsigned)grid, kThreads, Layout<DP>::kBytes, stream>>>(maps, p, ntiles, stat_tiles(p), ch);
   e = cudaGetLastError();
   if (e != cudaSuccess || DQ || !ch.sink_tiles) return e;
-  sink_sum_kernel<<<(unsigned)((pairs * ch.sink_tiles * kBM + 7) / 8), 256, 0, stream>>>(p, ch);
+  const int sinks = std::min(p.sinks, p.T);
+  sink_sum_kernel<<<(unsigned)((pairs * sinks + 7) / 8), 256, 0, stream>>>(p, ch, sinks);
   return cudaGetLastError();
 }
 

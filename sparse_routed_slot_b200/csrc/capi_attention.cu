@@ -173,8 +173,13 @@ rsm::AttnParams paged_params(const rsm_paged_args& a) {
   return p;
 }
 
-size_t paged_bytes(const rsm::AttnParams& p) {
-  if (p.splits <= 1) return 0;
+// Whether the blocks that share a row's keys leave partial results to a second kernel.
+bool has_parts(const rsm::AttnParams& p, rsm_dtype dtype) {
+  return p.splits > 1 && !(rsm::attn_decode_supported(p, dtype) && rsm::attn_decode_joins(p));
+}
+
+size_t paged_bytes(const rsm::AttnParams& p, rsm_dtype dtype) {
+  if (!has_parts(p, dtype)) return 0;
   const size_t rows = (size_t)p.T * p.H;
   return up256((size_t)p.splits * rows * p.D * sizeof(float)) + up256((size_t)p.splits * rows * sizeof(float));
 }
@@ -282,7 +287,7 @@ rsm_status rsm_paged_append(const rsm_paged_append_args* a, void* stream) {
 size_t rsm_paged_workspace_size(const rsm_paged_args* a) {
   if (check_paged(a) != RSM_OK) return (size_t)-1;
   if ((int64_t)a->N * a->H == 0 || a->B == 0 || a->max_q == 0) return 0;
-  return paged_bytes(paged_params(*a));
+  return paged_bytes(paged_params(*a), a->dtype);
 }
 
 rsm_status rsm_paged_forward(const rsm_paged_args* a, void* stream) {
@@ -291,8 +296,9 @@ rsm_status rsm_paged_forward(const rsm_paged_args* a, void* stream) {
   if (s != RSM_OK) return s;
   if ((int64_t)a->N * a->H == 0 || a->B == 0 || a->max_q == 0) return RSM_OK;
   rsm::AttnParams p = paged_params(*a);
-  if ((s = check_workspace(a->workspace, a->workspace_bytes, paged_bytes(p))) != RSM_OK) return s;
-  if (p.splits > 1) {
+  if ((s = check_workspace(a->workspace, a->workspace_bytes, paged_bytes(p, a->dtype))) != RSM_OK) return s;
+  const bool parts = has_parts(p, a->dtype);
+  if (parts) {
     p.part_o = static_cast<float*>(a->workspace);
     p.part_lse = reinterpret_cast<float*>(static_cast<char*>(a->workspace) +
                                           up256((size_t)p.splits * p.T * p.H * p.D * sizeof(float)));
@@ -302,7 +308,7 @@ rsm_status rsm_paged_forward(const rsm_paged_args* a, void* stream) {
                       ? rsm::launch_check_finite(a->q, (int64_t)a->N * a->H * a->D, a->dtype, st)
                       : cudaSuccess;
   if (e == cudaSuccess) e = launch_forward(p, a->dtype, st);
-  if (e == cudaSuccess && p.splits > 1) e = rsm::launch_attn_combine(p, a->dtype, st);
+  if (e == cudaSuccess && parts) e = rsm::launch_attn_combine(p, a->dtype, st);
   return finish(e, "rsm_paged_forward");
 }
 

@@ -82,6 +82,8 @@ cudaError_t launch_attn_tc(const AttnParams& p, cudaStream_t stream);
 // Few query rows per key/value head (attn_decode.cu): bf16, paged, single tokens above all.
 bool attn_decode_supported(const AttnParams& p, rsm_dtype dtype);
 int attn_decode_splits(const AttnParams& p);
+// Whether p.splits blocks join in the kernel (no partial results, no second kernel).
+bool attn_decode_joins(const AttnParams& p);
 cudaError_t launch_attn_decode(const AttnParams& p, cudaStream_t stream);
 // Its gradients (attn_tc_backward.cu), dense only; the workspace holds attn_tc_backward_bytes(p) bytes.
 size_t attn_tc_backward_bytes(const AttnParams& p);

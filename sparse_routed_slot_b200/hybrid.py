@@ -151,9 +151,10 @@ def window_backward(q, k, v, o, lse, dO, window: int, sinks: int = 0, scale=None
 class WindowFunction(torch.autograd.Function):
     """Window attention as an autograd function: apply(q, k, v, window, sinks=0, scale=None) -> o.
 
-    Recording a training step into a CUDA graph follows torch's own rule: no graph of the same
-    leaves built outside the capture may be alive meanwhile, or the capture fails. window_forward and
-    window_backward carry no such state."""
+    Recording a training step into a CUDA graph follows torch's own rule for every autograd function: no
+    eager graph of the same leaves may be alive during the capture (torch then touches their old stream from
+    its backward thread, which fails the capture and can end the process). window_forward and
+    window_backward, called directly, carry no such state."""
 
     @staticmethod
     def forward(ctx, q, k, v, window, sinks=0, scale=None):

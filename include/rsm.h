@@ -289,6 +289,8 @@ RSM_API rsm_status rsm_backward(const rsm_backward_args* args, void* stream);
  *   q       [B,T,H,D] in dtype;  k, v [B,T,Hkv,D] in dtype
  *   o       [B,T,H,D] in dtype (required)
  *   lse     [B,T,H] fp32, or NULL to skip: natural logarithm of the row's sum (the backward reads it)
+ *   o_low   [B,T,H,D] bf16, or NULL to skip (bf16 inputs only): what rounding left of o, that is the
+ *           unrounded result minus o, for the backward
  *   Scores, softmax statistics and sums are fp32. With bf16 inputs the softmax weights are rounded
  *   to bf16 for the product with v; with fp32 inputs everything is fp32.
  *   q, k and v must be finite (checked when RSM_FLAG_VALIDATE is set): a weight of zero does not
@@ -306,6 +308,7 @@ typedef struct rsm_window_args {
   const void* v;
   void* o;
   float* lse;
+  void* o_low;
   int flags; /* RSM_FLAG_* */
 } rsm_window_args;
 
@@ -316,7 +319,9 @@ RSM_API rsm_status rsm_window_forward(const rsm_window_args* args, void* stream)
  * p_ij = e^{s_ij - lse_i} and ds_ij = p_ij (dO_i.v_j - delta_i):
  *   dq_i = scale sum_j ds_ij k_j;  dk_j = scale sum_i ds_ij q_i;  dv_j = sum_i p_ij dO_i
  * the sums of dk and dv running over the query heads that share the key/value head, too.
- *   q, k, v, o, lse: the forward's inputs and outputs;  dO [B,T,H,D] in dtype
+ *   q, k, v, o, lse, o_low: the forward's inputs and outputs;  dO [B,T,H,D] in dtype. o_low may be NULL:
+ *     delta is then formed with the rounded o, which a row of few keys shows in dq and dk (their error
+ *     doubles there; with o_low it stays that of rounding ds and the results).
  *   dq [B,T,H,D], dk, dv [B,T,Hkv,D] in dtype (each may be NULL to skip it)
  *   workspace: at least rsm_window_backward_workspace_size(args) bytes (256-byte aligned); its
  *     contents are not preserved.
@@ -333,6 +338,7 @@ typedef struct rsm_window_backward_args {
   const void* v;
   const void* o;
   const float* lse;
+  const void* o_low;
   const void* dO;
   void* dq;
   void* dk;

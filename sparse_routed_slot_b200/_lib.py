@@ -69,13 +69,13 @@ class BackwardArgs(ctypes.Structure):
 class WindowArgs(ctypes.Structure):
     _fields_ = [("B", _int), ("T", _int), ("H", _int), ("Hkv", _int), ("D", _int), ("window", _int), ("sinks", _int),
                 ("dtype", _int), ("scale", _float), ("q", _vp), ("k", _vp), ("v", _vp), ("o", _vp), ("lse", _vp),
-                ("flags", _int)]
+                ("o_low", _vp), ("flags", _int)]
 
 
 class WindowBackwardArgs(ctypes.Structure):
     _fields_ = [("B", _int), ("T", _int), ("H", _int), ("Hkv", _int), ("D", _int), ("window", _int), ("sinks", _int),
                 ("dtype", _int), ("scale", _float), ("q", _vp), ("k", _vp), ("v", _vp), ("o", _vp), ("lse", _vp),
-                ("dO", _vp), ("dq", _vp), ("dk", _vp), ("dv", _vp), ("workspace", _vp), ("workspace_bytes", _size),
+                ("o_low", _vp), ("dO", _vp), ("dq", _vp), ("dk", _vp), ("dv", _vp), ("workspace", _vp), ("workspace_bytes", _size),
                 ("flags", _int)]
 
 

@@ -241,6 +241,10 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const AttnParams p,
         Out<float>::st4(p.part_o + (split * total + at) * D + d, a.x * inv, a.y * inv, a.z * inv, a.w * inv);
       else
         Out<T>::st4(static_cast<T*>(p.o) + at * D + d, a.x * inv, a.y * inv, a.z * inv, a.w * inv);
+      if (sizeof(T) == 2 && p.o_low) {
+        auto low = [&](float x) { return x - __bfloat162float(__float2bfloat16_rn(x)); };
+        Out<T>::st4(static_cast<T*>(p.o_low) + at * D + d, low(a.x * inv), low(a.y * inv), low(a.z * inv), low(a.w * inv));
+      }
     }
     if (tx == 0) {
       if (p.splits > 1) p.part_lse[split * total + at] = lse;
@@ -418,7 +422,7 @@ template <typename T> __global__ void __launch_bounds__(256) cut_sum_kernel(cons
 
 // delta = dO . o, a warp per row.
 template <typename T>
-__global__ void __launch_bounds__(256) delta_kernel(const T* dO, const T* o, float* delta, int64_t rows, int D) {
+__global__ void __launch_bounds__(256) delta_kernel(const T* dO, const T* o, const T* o_low, float* delta, int64_t rows, int D) {
   const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   if (row >= rows) return;
   const int lane = threadIdx.x & 31;
@@ -427,6 +431,12 @@ __global__ void __launch_bounds__(256) delta_kernel(const T* dO, const T* o, flo
     float a[4], x[4];
     In<T>::ld4(dO + row * D + d, a);
     In<T>::ld4(o + row * D + d, x);
+    if (o_low) {
+      float low[4];
+      In<T>::ld4(o_low + row * D + d, low);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] += low[i];
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) sum = fmaf(a[i], x[i], sum);
   }
@@ -614,11 +624,12 @@ cudaError_t launch_attn_delta(const AttnParams& p, rsm_dtype dtype, cudaStream_t
   const int64_t rows = all_rows(p);
   const unsigned grid = (unsigned)((rows + 7) / 8);
   if (dtype == RSM_F32)
-    delta_kernel<float><<<grid, 256, 0, stream>>>(static_cast<const float*>(p.dO), static_cast<const float*>(p.o),
+    delta_kernel<float><<<grid, 256, 0, stream>>>(static_cast<const float*>(p.dO), static_cast<const float*>(p.o), nullptr,
                                                   p.delta, rows, p.D);
   else
     delta_kernel<__nv_bfloat16><<<grid, 256, 0, stream>>>(static_cast<const __nv_bfloat16*>(p.dO),
-                                                          static_cast<const __nv_bfloat16*>(p.o), p.delta, rows, p.D);
+                                                          static_cast<const __nv_bfloat16*>(p.o),
+                                                          static_cast<const __nv_bfloat16*>(p.o_low), p.delta, rows, p.D);
   return cudaGetLastError();
 }
 

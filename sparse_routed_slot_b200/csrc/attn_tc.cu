@@ -11,6 +11,12 @@
 // The reference m of a row is its first tile's maximum and moves only when the running one has passed it by
 // 2^32: fp32 sums and bf16 weights keep their relative precision at any scale, so O is next to never
 // rescaled (at 2^8, a warp rescaled every fourth tile of 2048 random keys, at 1600 cycles).
+// As the reference is not the row's maximum, the largest weight is rounded too. The dense form therefore
+// divides by the sum of the rounded weights: what is left of their rounding in o is sum eta_j p_j (v_j - o),
+// which vanishes with a single large weight. Divided by the unrounded sum, a peaked row kept eta v, and
+// delta = dO . o carried it into ds, which is small there (window of 3 to 9 keys: dq off by 3.2e-3 of its norm
+// instead of 2.6e-3). lse is the unrounded sum's. It costs 3 % (65536 tokens 609 -> 628 us). Nothing
+// differentiates the paged form, which keeps the one sum.
 //
 // Each query tile has two S buffers, so that S of the next keys is there when the rows' threads finish
 // with this one: the products, not the chain S -> P -> O -> S, set the pace (with one 128-key buffer per
@@ -45,7 +51,7 @@ constexpr int kCopyWarp = 8, kMmaWarp = 9;  // and kMmaWarp + 1
 constexpr float kSlack = 32.f;  // how far (log2) the running maximum may pass the reference
 
 struct Maps {
-  CUtensorMap q, k, v, o;
+  CUtensorMap q, k, v, o, o_low;
 };
 
 template <int DP> struct Layout {
@@ -260,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32);
     const uint32_t tS = tc::tmem_addr(tb, lane_base, t * 128), tO = tc::tmem_addr(tb, lane_base, 256 + t * DP);
     const float scale2 = p.scale * kLog2e;
-    float m = kNegInf, l = 0.f;
+    float m = kNegInf, l = 0.f, lr = 0.f;  // sums of the weights, and of the rounded ones
     int done = 0;
     bool ok = true;
     // The warps of both tiles that share a scheduler form their weights in turn: see above.
@@ -329,6 +335,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         tc::tmem_fence_after();
         const float f = move ? ex2(m - top) : 1.f;
         l *= f;
+        lr *= f;
 #pragma unroll 1
         for (int c = 0; c < DP; c += 16) {
           float o[16];
@@ -361,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       if (ok) {
         const float ref = m == kNegInf ? 0.f : m;
         const float2 s2 = make_float2(scale2, scale2), r2 = make_float2(-ref, -ref);
-        float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
+        float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0, low0 = sum0, low1 = sum0;
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
           float w[8];
@@ -372,11 +379,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             e.y = ex2(e.y);
             if (c & 1) sum1 = add2(sum1, e);
             else sum0 = add2(sum0, e);
-            w[c] = __uint_as_float(pack_bf16(e.x, e.y));
+            const uint32_t u = pack_bf16(e.x, e.y);
+            if (!PAGED) {
+              const float2 rounded = make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+              if (c & 1) low1 = add2(low1, rounded);
+              else low0 = add2(low0, rounded);
+            }
+            w[c] = __uint_as_float(u);
           }
           tc::tmem_st8(tP + 8 * h, w);
         }
         l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
+        lr += (low0.x + low0.y) + (low1.x + low1.y);
       }
       if (t ? done + 1 < theirs : done < theirs) turn_pass(their_turn);
       if (ok) {
@@ -398,7 +412,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     const bool live = r < ntok * G;
     const int64_t at = (s.row0 + tok) * p.H + hk * G + r % G;
     const int64_t total = (int64_t)p.T * (PAGED ? 1 : p.B) * p.H;
-    const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;  // (a NaN stays one)
+    const float by = PAGED ? l : lr;
+    const float inv = by > 0.f ? 1.f / by : by == 0.f ? 0.f : by;  // (a NaN stays one)
     // Whole tiles go through the query tile's memory, which is done with, to a tensor store; so does the last
     // tile of a dense sequence, whose rows behind the end the store leaves out. Behind the end of a paged one
     // stand the next sequence's rows.
@@ -413,6 +428,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
           tc::tma_store_4d(&maps.o, to + c * (kBM * 128), 64 * c, hk * G, (int)first, PAGED ? 0 : b);
         tc::bulk_commit_group();
         tc::bulk_wait_read_all();
+      }
+      if (!PAGED && p.o_low) {
+        group_sync(9 + t, 128);  // the tile is read out
+        if (ok) stage_row_low<DP>(to, r, tO, inv);
+        tc::fence_async_smem();
+        group_sync(9 + t, 128);
+        if (ok && r == 0) {
+          for (int c = 0; c < kBlocks; ++c)
+            tc::tma_store_4d(&maps.o_low, to + c * (kBM * 128), 64 * c, hk * G, tok0 + t * tok_tile, b);
+          tc::bulk_commit_group();
+          tc::bulk_wait_read_all();
+        }
       }
     } else if (ok && ntok > 0) {
 #pragma unroll 1
@@ -499,7 +526,9 @@ cudaError_t launch_attn_tc(const AttnParams& p, cudaStream_t stream) {
   const uint64_t T = p.T, B = paged ? 1 : p.B;
   const int tok = token_tile(p);
   bool ok = true;
-  for (auto [m, base] : {std::pair<CUtensorMap*, const void*>{&maps.q, p.q}, {&maps.o, p.o}})
+  // (without o_low nothing is stored through its map)
+  for (auto [m, base] : {std::pair<CUtensorMap*, const void*>{&maps.q, p.q}, {&maps.o, p.o},
+                         {&maps.o_low, p.o_low ? p.o_low : p.o}})
     ok = ok && make_map_bf16(m, base, {D, H, T, B}, {D, H * D, T * H * D}, {64, (uint32_t)p.G, (uint32_t)tok, 1});
   if (paged) {
     const uint64_t page = p.page, pages = p.num_pages;

@@ -64,6 +64,27 @@ template <int NC> RSM_DEV void stage_row(unsigned char* tile, int r, int c0, uin
     }
   }
 }
+// What that rounding left, as bf16, into such a tile.
+template <int NC> RSM_DEV void stage_row_low(unsigned char* tile, int r, uint32_t tmem, float scale) {
+#pragma unroll 1
+  for (int c = 0; c < NC; c += 32) {
+    float x[32];
+    tc::tmem_ld32(tmem + c, x);
+    tc::tmem_wait_ld();
+#pragma unroll
+    for (int e = 0; e < 32; ++e) {
+      x[e] *= scale;
+      x[e] -= __bfloat162float(__float2bfloat16_rn(x[e]));
+    }
+#pragma unroll
+    for (int e = 0; e < 32; e += 8) {
+      const int k = (c + e) >> 3;
+      *reinterpret_cast<uint4*>(tile + (k >> 3) * (128 * 128) + r * 128 + (((k & 7) ^ (r & 7)) << 4)) =
+          make_uint4(pack_bf16(x[e], x[e + 1]), pack_bf16(x[e + 2], x[e + 3]), pack_bf16(x[e + 4], x[e + 5]),
+                     pack_bf16(x[e + 6], x[e + 7]));
+    }
+  }
+}
 // The same columns straight to memory, 16 bytes at a time.
 template <int NC> RSM_DEV void store_row(__nv_bfloat16* to, uint32_t tmem, float scale, int cols, bool live) {
 #pragma unroll 1

@@ -8,6 +8,7 @@
 //   S = A1 B1^T, E = A2 B2^T             fp32 in TMEM, a thread per row of A
 //   P = 2^(S' - lse), Z = P (E - delta)  -> bf16 over S and E (rounded here: the next products take bf16)
 //   G2 += Z B1  (dk or dq),  G1 += P B2  (dv; not in the dq run)
+// delta = dO . o is formed with what rounding left of o where the forward kept it.
 // S and E have two buffers each and two groups of 128 threads take the steps in turn, so S and E of the
 // next step are there when a group comes back, and one group's exponentials run beside the other's loads.
 // The tiles of 64 leave room for four stages of B: with 128 and two, each step waited for its copies
@@ -396,14 +397,18 @@ __global__ void __launch_bounds__(256) stat_kernel(const AttnParams p, int64_t r
   const int lane = threadIdx.x & 15;
   const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(p.dO) + row * p.D;
   const __nv_bfloat16* y = static_cast<const __nv_bfloat16*>(p.o) + row * p.D;
+  const __nv_bfloat16* z = p.o_low ? static_cast<const __nv_bfloat16*>(p.o_low) + row * p.D : nullptr;
   float sum = 0.f;
   for (int d = lane * 8; d < p.D; d += 128) {
     const uint4 a = *reinterpret_cast<const uint4*>(x + d), c = *reinterpret_cast<const uint4*>(y + d);
-    const uint32_t u[4] = {a.x, a.y, a.z, a.w}, v[4] = {c.x, c.y, c.z, c.w};
+    uint4 low = make_uint4(0u, 0u, 0u, 0u);
+    if (z) low = *reinterpret_cast<const uint4*>(z + d);
+    const uint32_t u[4] = {a.x, a.y, a.z, a.w}, v[4] = {c.x, c.y, c.z, c.w}, w[4] = {low.x, low.y, low.z, low.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      sum = fmaf(__uint_as_float(u[i] << 16), __uint_as_float(v[i] << 16), sum);
-      sum = fmaf(__uint_as_float(u[i] & 0xffff0000u), __uint_as_float(v[i] & 0xffff0000u), sum);
+      sum = fmaf(__uint_as_float(u[i] << 16), __uint_as_float(v[i] << 16) + __uint_as_float(w[i] << 16), sum);
+      sum = fmaf(__uint_as_float(u[i] & 0xffff0000u),
+                 __uint_as_float(v[i] & 0xffff0000u) + __uint_as_float(w[i] & 0xffff0000u), sum);
     }
   }
 #pragma unroll

@@ -65,6 +65,12 @@ rsm_status check_window(int B, int T, int H, int Hkv, int D, int window, int sin
   return RSM_OK;
 }
 
+rsm_status check_low(const void* o_low, rsm_dtype dtype) {
+  MAY_PTR(o_low, "o_low");
+  if (o_low && dtype != RSM_BF16) return fail(RSM_ERR_INVALID_ARG, "o_low goes with bf16 only");
+  return RSM_OK;
+}
+
 // Launches of 2^31 blocks and more are refused (8 rows per block in the row kernels).
 rsm_status check_rows(int64_t rows) {
   if (rows / 8 > 0x7fffff00) return fail(RSM_ERR_UNSUPPORTED, "too many rows");
@@ -116,6 +122,7 @@ rsm_status check_window_backward(const rsm_window_backward_args* a) {
   if ((int64_t)a->B * a->T * a->H == 0) return RSM_OK;
   NEED_PTR(a->q, "q"); NEED_PTR(a->k, "k"); NEED_PTR(a->v, "v");
   NEED_PTR(a->o, "o"); NEED_PTR(a->lse, "lse"); NEED_PTR(a->dO, "dO");
+  if ((s = check_low(a->o_low, a->dtype)) != RSM_OK) return s;
   MAY_PTR(a->dq, "dq"); MAY_PTR(a->dk, "dk"); MAY_PTR(a->dv, "dv");
   return RSM_OK;
 }
@@ -226,12 +233,14 @@ rsm_status rsm_window_forward(const rsm_window_args* a, void* stream) {
   if ((int64_t)a->B * a->T * a->H == 0) return RSM_OK;
   NEED_PTR(a->q, "q"); NEED_PTR(a->k, "k"); NEED_PTR(a->v, "v"); NEED_PTR(a->o, "o");
   MAY_PTR(a->lse, "lse");
+  if ((s = check_low(a->o_low, a->dtype)) != RSM_OK) return s;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e = a->flags & RSM_FLAG_VALIDATE ? validate_qkv(*a, st) : cudaSuccess;
   if (e == cudaSuccess) {
     rsm::AttnParams p = window_params(*a);
     p.o = a->o;
     p.lse = a->lse;
+    p.o_low = a->o_low;
     e = launch_forward(p, a->dtype, st);
   }
   return finish(e, "rsm_window_forward");
@@ -257,6 +266,7 @@ rsm_status rsm_window_backward(const rsm_window_backward_args* a, void* stream) 
   rsm::AttnParams p = window_params(*a);
   p.o = const_cast<void*>(a->o);
   p.lse = const_cast<float*>(a->lse);
+  p.o_low = const_cast<void*>(a->o_low);
   p.dO = a->dO;
   p.dq = a->dq; p.dk = a->dk; p.dv = a->dv;
   if (e == cudaSuccess && rsm::attn_tc_supported(p, a->dtype)) {

@@ -54,6 +54,7 @@ struct AttnParams {
   const void* v;
   void* o;
   float* lse;
+  void* o_low;        // what rounding left of o, or null
   const int32_t* table;
   const int32_t* cu_q;
   const int32_t* kv_len;

@@ -107,33 +107,38 @@ def _window_args(cls, q, k, v, window, sinks, scale, validate):
     return a, dtype, shape, kshape, index
 
 
-def window_forward(q, k, v, window: int, sinks: int = 0, scale=None, *, lse: bool = False, validate: bool = False,
-                   out=None):
+def window_forward(q, k, v, window: int, sinks: int = 0, scale=None, *, lse: bool = False, low: bool = False,
+                   validate: bool = False, out=None):
     """Causal attention over the last `window` keys and the first `sinks`. q [B,T,H,D]; k, v
     [B,T,Hkv,D] with Hkv dividing H; float32 or bfloat16. scale defaults to 1/sqrt(D).
 
-    Returns dict(o [B,T,H,D] in q's dtype, lse [B,T,H] fp32 or None). `out` may supply preallocated
-    tensors under the same keys."""
+    Returns dict(o [B,T,H,D] in q's dtype, lse [B,T,H] fp32 or None, low like o or None: with `low`, what
+    rounding left of a bfloat16 o, for window_backward). `out` may supply preallocated tensors under the
+    same keys."""
     a, dtype, shape, _, index = _window_args(_lib.WindowArgs, q, k, v, window, sinks, scale, validate)
-    o = ls = None
+    o = ls = lo = None
     if out:
-        o, ls = out.get("o"), out.get("lse")
+        o, ls, lo = out.get("o"), out.get("lse"), out.get("low")
     if o is None:
         o = torch.empty_like(q)
     if ls is None and lse:
         ls = torch.empty(shape[:3], dtype=torch.float32, device=q.device)
+    if lo is None and low and dtype is torch.bfloat16:
+        lo = torch.empty_like(q)
     a.o, a.lse = _ptr(o, "o", dtype, shape, index), _ptr(ls, "lse", torch.float32, shape[:3], index)
+    a.o_low = _ptr(lo, "low", dtype, shape, index)
     _run(_lib.load().rsm_window_forward, a, index)
-    return {"o": o, "lse": ls}
+    return {"o": o, "lse": ls, "low": lo}
 
 
-def window_backward(q, k, v, o, lse, dO, window: int, sinks: int = 0, scale=None, *, need=(True, True, True),
-                    validate: bool = False, out=None, workspace=None):
-    """Gradients of window_forward: its inputs, its o and lse, and dO [B,T,H,D] in q's dtype.
+def window_backward(q, k, v, o, lse, dO, window: int, sinks: int = 0, scale=None, *, low=None,
+                    need=(True, True, True), validate: bool = False, out=None, workspace=None):
+    """Gradients of window_forward: its inputs, its o, lse and (if kept) low, and dO [B,T,H,D] in q's dtype.
     Returns dict(dq, dk, dv) in q's dtype (None where `need` says so)."""
     a, dtype, shape, kshape, index = _window_args(_lib.WindowBackwardArgs, q, k, v, window, sinks, scale, validate)
     a.o, a.dO = _given(o, "o", dtype, shape, index), _given(dO, "dO", dtype, shape, index)
     a.lse = _given(lse, "lse", torch.float32, shape[:3], index)
+    a.o_low = _ptr(low, "low", dtype, shape, index)
     got = {}
     for name, like, size, wanted in zip(("dq", "dk", "dv"), (q, k, v), (shape, kshape, kshape), need):
         g = None
@@ -158,16 +163,16 @@ class WindowFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, q, k, v, window, sinks=0, scale=None):
-        r = window_forward(q, k, v, window, sinks, scale, lse=True)
-        ctx.save_for_backward(q, k, v, r["o"], r["lse"])
+        r = window_forward(q, k, v, window, sinks, scale, lse=True, low=True)
+        ctx.save_for_backward(q, k, v, r["o"], r["lse"], r["low"])
         ctx.how = (window, sinks, scale)
         return r["o"]
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dO):
-        q, k, v, o, lse = ctx.saved_tensors
-        g = window_backward(q, k, v, o, lse, dO.contiguous(), *ctx.how, need=ctx.needs_input_grad[:3])
+        q, k, v, o, lse, low = ctx.saved_tensors
+        g = window_backward(q, k, v, o, lse, dO.contiguous(), *ctx.how, low=low, need=ctx.needs_input_grad[:3])
         return g["dq"], g["dk"], g["dv"], None, None, None
 
 

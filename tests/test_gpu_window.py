@@ -99,21 +99,41 @@ def test_autograd_and_skipped_gradients(rsm, dtype):
     leaves = [t.clone().requires_grad_(True) for t in (q, k, v)]
     o = rsm.WindowFunction.apply(*leaves, 60, 2)
     (o.float() * do.float()).sum().backward()
-    r = rsm.window_forward(q, k, v, 60, 2, lse=True)
-    g = rsm.window_backward(q, k, v, r["o"], r["lse"], do, 60, 2)
-    assert torch.equal(o, r["o"])
+    r = rsm.window_forward(q, k, v, 60, 2, lse=True, low=True)
+    g = rsm.window_backward(q, k, v, r["o"], r["lse"], do, 60, 2, low=r["low"])
+    assert torch.equal(o, r["o"]) and (r["low"] is None) == (dtype == F32)
     for x, n in zip(leaves, ("dq", "dk", "dv")):
         assert torch.equal(x.grad, g[n])
     for keep in range(3):
         need = [i == keep for i in range(3)]
-        one = rsm.window_backward(q, k, v, r["o"], r["lse"], do, 60, 2, need=need)
+        one = rsm.window_backward(q, k, v, r["o"], r["lse"], do, 60, 2, low=r["low"], need=need)
         for i, n in enumerate(("dq", "dk", "dv")):
             assert (one[n] is None) if not need[i] else torch.equal(one[n], g[n])
     # an expanded output gradient (a plain sum's) is not contiguous
     leaves = [t.clone().requires_grad_(True) for t in (q, k, v)]
     rsm.WindowFunction.apply(*leaves, 60, 2).sum().backward()
-    ones = rsm.window_backward(q, k, v, r["o"], r["lse"], torch.ones_like(do), 60, 2)
+    ones = rsm.window_backward(q, k, v, r["o"], r["lse"], torch.ones_like(do), 60, 2, low=r["low"])
     assert all(torch.equal(x.grad, ones[n]) for x, n in zip(leaves, ("dq", "dk", "dv")))
+
+
+@pytest.mark.parametrize("shape", [(2, 129, 6, 2, 64, 5, 1), (1, 300, 4, 4, 128, 9, 0), (1, 70, 2, 1, 256, 4, 2),
+                                   (1, 90, 3, 3, 80, 3, 1)])
+def test_what_rounding_left(rsm, shape):
+    """o + low is o to 16 bits more or less, and with it the gradients of rows of few keys keep two of their three
+    roundings (ds, and the result: 2^-8 / sqrt(3) rms each; the fp32 arithmetic is far below). Both are uniform in the
+    worst case only; their usual size, 0.0017 each, leaves room for what the weights' rounding keeps in o."""
+    B, T, H, Hkv, D, W, S = shape
+    q, k, v, do = inputs(B, T, H, Hkv, D, BF16, seed=D)
+    r = rsm.window_forward(q, k, v, W, S, lse=True, low=True)
+    assert torch.equal(r["o"], rsm.window_forward(q, k, v, W, S)["o"])
+    g = rsm.window_backward(q, k, v, r["o"], r["lse"], do, W, S, low=r["low"])
+    want = hybrid.window(q, k, v, W, S, 1 / math.sqrt(D), do, *roundings(BF16))
+    # the softmax weights' rounding stays in o, the result's own is gone but for half a step of the rest
+    within("o + low", r["o"].double() + r["low"].double(), *want["o"], rms=False)
+    off = lambda x, y: float((x - y).norm() / y.norm())  # noqa: E731
+    assert off(r["o"].double() + r["low"].double(), want["o"][0]) < off(r["o"].double(), want["o"][0])
+    for n in ("dq", "dk"):
+        assert off(g[n].double(), want[n][0]) <= 2.0 ** -8 * (2 / 3) ** 0.5, n
 
 
 def test_empty_and_refused(rsm):
@@ -132,6 +152,9 @@ def test_empty_and_refused(rsm):
             rsm.window_forward(x, x, x, **kw)
     with pytest.raises(ValueError):
         rsm.window_backward(x, x, x, x, torch.zeros(1, 4, 2, device="cuda"), x.float(), 3)
+    y = x.float()
+    with pytest.raises(rsm.RSMError):  # nothing is rounded in fp32
+        rsm.window_forward(y, y, y, 3, out={"low": torch.zeros_like(y)})
 
 
 def test_validate_reports_infinities(rsm):

@@ -40,7 +40,8 @@ def attend(q, k, v, at, window, sinks, scale, do=None, u=0.0, uo=0.0):
     worst = es.masked_fill(~seen, 0.0).amax(2)
     rp = es + worst[..., None] + (4 * mag[..., None] + L + 64) * U32 + 2.0 ** -20
     o = torch.einsum("hnl,lhd->nhd", p, vv)
-    eo = torch.einsum("hnl,lhd->nhd", p * (rp + u + (L + 8) * U32), vv.abs()) + (uo + 2 * U32) * o.abs()
+    # rounded weights move o by sum eta p v over the plain sum of weights, by sum eta p (v - o) over their own
+    eo = torch.einsum("hnl,lhd->nhd", p * (rp + u + (L + 8) * U32), vv.abs()) + (u + uo + 2 * U32) * o.abs()
     out = {"o": (o, eo), "lse": (lse.T, (worst + (8 * mag + 64) * U32 + 2.0 ** -20).T)}
     if do is None:
         return out

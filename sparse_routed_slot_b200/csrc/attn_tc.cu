@@ -15,7 +15,7 @@
 // divides by the sum of the rounded weights: what is left of their rounding in o is sum eta_j p_j (v_j - o),
 // which vanishes with a single large weight. Divided by the unrounded sum, a peaked row kept eta v, and
 // delta = dO . o carried it into ds, which is small there (window of 3 to 9 keys: dq off by 3.2e-3 of its norm
-// instead of 2.6e-3). lse is the unrounded sum's. It costs 3 % (65536 tokens 609 -> 628 us). Nothing
+// instead of 2.6e-3). lse is the unrounded sum's. It costs 3 % (32768 tokens, 16 heads of 128: 609 -> 628 us). Nothing
 // differentiates the paged form, which keeps the one sum.
 //
 // Each query tile has two S buffers, so that S of the next keys is there when the rows' threads finish

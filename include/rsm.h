@@ -296,7 +296,8 @@ RSM_API rsm_status rsm_backward(const rsm_backward_args* args, void* stream);
  *   q, k and v must be finite (checked when RSM_FLAG_VALIDATE is set): a weight of zero does not
  *   hide an infinity in v.
  *   Supported: 8 <= D <= 256 with D % 8 == 0, Hkv dividing H with H / Hkv <= 64, window >= 1,
- *   sinks >= 0, scale > 0 and finite, T*H < 2^31. B, T or H may be 0 (nothing is launched).
+ *   sinks >= 0, scale > 0 and finite, T*H < 2^31. B, T or H may be 0 (nothing is launched). Outputs
+ *   must not alias inputs or one another.
  * ------------------------------------------------------------------------------------------- */
 typedef struct rsm_window_args {
   int B, T, H, Hkv, D;
@@ -326,7 +327,8 @@ RSM_API rsm_status rsm_window_forward(const rsm_window_args* args, void* stream)
  *   workspace: at least rsm_window_backward_workspace_size(args) bytes (256-byte aligned); its
  *     contents are not preserved.
  *   The gradients are the same, bit for bit, from call to call: no sum is left to the order in
- *   which blocks finish. Sizes as rsm_window_forward.
+ *   which blocks finish. Sizes as rsm_window_forward; with H = 0, dk and dv are zeros. Outputs must
+ *   not alias inputs or one another.
  * ------------------------------------------------------------------------------------------- */
 typedef struct rsm_window_backward_args {
   int B, T, H, Hkv, D;
@@ -395,7 +397,8 @@ RSM_API rsm_status rsm_paged_append(const rsm_paged_append_args* args, void* str
  *   does not matter (it may be NaN); what it holds in front of it must be finite.
  *   workspace: at least rsm_paged_workspace_size(args) bytes (256-byte aligned; may be NULL when
  *     that is 0): partial results of long caches that several blocks share.
- *   Sizes as rsm_window_forward; page_size >= 1, N*H < 2^31, table_width*page_size < 2^31.
+ *   Sizes as rsm_window_forward; page_size >= 1, N*H and max_q*H < 2^31, table_width*page_size < 2^31.
+ *   Outputs must not alias inputs or one another.
  * ------------------------------------------------------------------------------------------- */
 typedef struct rsm_paged_args {
   int B, N, max_q, H, Hkv, D;

@@ -255,10 +255,15 @@ rsm_status rsm_window_backward(const rsm_window_backward_args* a, void* stream) 
   rsm::report_error(RSM_OK, "");
   rsm_status s = check_window_backward(a);
   if (s != RSM_OK) return s;
-  if ((int64_t)a->B * a->T * a->H == 0) return RSM_OK;
-  if ((s = check_workspace(a->workspace, a->workspace_bytes, window_backward_bytes(*a))) != RSM_OK) return s;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
+  if ((int64_t)a->B * a->T * a->H == 0) {  // no query heads: the keys' gradients are empty sums
+    const size_t bytes = (size_t)a->B * a->T * a->Hkv * a->D * (a->dtype == RSM_F32 ? 4 : 2);
+    if (a->dk && bytes) e = cudaMemsetAsync(a->dk, 0, bytes, st);
+    if (a->dv && bytes && e == cudaSuccess) e = cudaMemsetAsync(a->dv, 0, bytes, st);
+    return finish(e, "rsm_window_backward (no query heads)");
+  }
+  if ((s = check_workspace(a->workspace, a->workspace_bytes, window_backward_bytes(*a))) != RSM_OK) return s;
   if (a->flags & RSM_FLAG_VALIDATE) {
     e = validate_qkv(*a, st);
     if (e == cudaSuccess) e = rsm::launch_check_finite(a->dO, (int64_t)a->B * a->T * a->H * a->D, a->dtype, st);

@@ -136,6 +136,17 @@ def test_what_rounding_left(rsm, shape):
         assert off(g[n].double(), want[n][0]) <= 2.0 ** -8 * (2 / 3) ** 0.5, n
 
 
+def test_no_query_heads(rsm):
+    """Keys and values that no query head reads: their gradients are empty sums."""
+    x, k = torch.zeros(1, 5, 0, 8, device="cuda", dtype=BF16), torch.zeros(1, 5, 2, 8, device="cuda", dtype=BF16)
+    r = rsm.window_forward(x, k, k, 3, lse=True)
+    out = {n: torch.full_like(k, float("nan")) for n in ("dk", "dv")}
+    g = rsm.window_backward(x, k, k, r["o"], r["lse"], x, 3, out=out)
+    assert g["dq"].numel() == 0 and not g["dk"].any() and not g["dv"].any()
+    one = rsm.window_backward(x, k, k, r["o"], r["lse"], x, 3, need=(True, False, True))
+    assert one["dk"] is None and not one["dv"].any()
+
+
 def test_empty_and_refused(rsm):
     for shape in ((0, 5, 2, 8), (1, 0, 2, 8), (1, 5, 0, 8)):
         x = torch.zeros(shape, device="cuda", dtype=BF16)

@@ -385,7 +385,8 @@ template <int DP, int NQ> cudaError_t launch_as(const AttnParams& p, cudaStream_
 }  // namespace
 
 bool attn_decode_supported(const AttnParams& p, rsm_dtype dtype) {
-  return dtype == RSM_BF16 && p.table && (int64_t)p.max_q * p.G <= 16;
+  // (a cache of no pages has no address to copy from)
+  return dtype == RSM_BF16 && p.table && p.num_pages > 0 && p.table_width > 0 && (int64_t)p.max_q * p.G <= 16;
 }
 
 // Blocks that share a sequence's keys: where sequences and heads alone are fewer than four blocks per SM,

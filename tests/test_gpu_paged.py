@@ -218,6 +218,24 @@ def test_shared_pages(rsm, dtype):
     c.check(rsm)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("new", [1, 40])
+@pytest.mark.parametrize("pages,width", [(0, 0), (0, 3), (4, 0)])
+def test_caches_without_pages(rsm, dtype, new, pages, width):
+    """No keys anywhere: zeros, nothing written, and lengths above zero reported."""
+    kc = torch.zeros(pages, 16, 2, 64, device="cuda", dtype=dtype)
+    table = torch.zeros(2, width, device="cuda", dtype=torch.int32)
+    cu = torch.tensor([0, new, 2 * new], device="cuda", dtype=torch.int32)
+    x, k = (torch.ones(2 * new, h, 64, device="cuda", dtype=dtype) for h in (4, 2))
+    for lens, status in (([0, 0], 0), ([new, 0], 7)):
+        n = torch.tensor(lens, device="cuda", dtype=torch.int32)
+        rsm.paged_append(k, k, kc, kc.clone(), table, cu, n)
+        assert rsm.device_status() == status
+        r = rsm.paged_forward(x, kc, kc, table, cu, n, new, lse=True)
+        assert rsm.device_status() == status
+        assert not r["o"].any() and (r["lse"] == float("-inf")).all() and not kc.any()
+
+
 def test_far_pages(rsm):
     """A cache whose last page lies past 2^31 elements and 2^32 bytes."""
     Hkv, D, page = 8, 128, 64

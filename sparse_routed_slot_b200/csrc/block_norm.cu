@@ -7,14 +7,22 @@
 //   dH = dh + r2 e - h r2^3 mean(e h),  dres = dH,  du = scale dH
 //   dg = du n act'(g),  f = du act(g) w_post,  dy = r1 f - y r1^3 mean(f y)
 //   dw_post = sum_rows du act(g) y r1,  dw_pre = sum_rows dx h r2
-// Everything is fp32, two values per instruction, between the loads and the stores; h is normalised before it is rounded, and the
-// backward forms it again from its inputs, so no rounded value enters a sum.
+// Everything is fp32, two values per instruction, between the loads and the stores; h is normalised before it
+// is rounded, and the backward forms it again from its inputs, so no rounded value enters a sum.
 //
-// A row stays in registers: TPR threads hold VEC * ITER values each, and the row crosses memory once
-// (bound: HBM bandwidth). The row sums go over shuffles and, past one warp, one exchange in shared
-// memory. In the backward each thread adds up its columns' weight gradients in registers over all of its
-// rows; the blocks' sums are joined by a second kernel in a fixed order (no atomics: the result does not
-// change from call to call).
+// A row stays on the SM: TPR threads hold VEC * ITER values each, and the row crosses memory once (bound: HBM
+// bandwidth). The row sums go over shuffles and, past one warp, one exchange in shared memory. In the backward
+// each thread adds up its columns' weight gradients in registers over all of its rows; the blocks' sums are
+// joined by a second kernel in a fixed order (no atomics: the result does not change from call to call).
+//
+// 2^25 values, us, forward / gradients (the copy rate: 51 / 82 bf16, 61 / 102 with fp32 y, 102 / 164 fp32):
+//   d           64         128        1024       2048       2500         4096       8192
+//   bf16        61 / 114   61 / 118   59 / 124   60 / 138    -  / 200    65 / 120   64 / 130
+//   fp32 y      75 / 144   75 / 146   70 / 163   72 / 161    -  / 198    78 / 144    -  / 163
+//   fp32       115 / 190  115 / 189  117 / 179  119 / 179    -  / 253   114 / 177  117 / 193
+// What is left is the chain of three row sums in the gradients (two in the forward) and, where d is not a
+// multiple of 8, bf16 pieces of 8 bytes. With the next row in registers instead of the ring (and 256 threads or
+// more, a power of two, per block) the gradients of bf16 took 318, 173, 163, 173, 308, 190 and 235.
 #include <algorithm>
 #include <type_traits>
 
@@ -24,8 +32,6 @@
 namespace rsm {
 
 namespace {
-
-constexpr int kMaxThreads = 512;
 
 // VEC values as they stand in memory (16 bytes, or 8, at a time).
 template <typename T, int VEC> struct Raw {
@@ -71,20 +77,26 @@ template <typename T, int VEC> RSM_DEV void store_vec(T* p, const float2 (&x)[VE
   }
 }
 
-// Sums of NV values over the TPR threads of a row (TPR a multiple of 32; every thread of the block
+// Sums of NV values over the TPR threads of a row (8, 16 or a multiple of 32; every thread of the block
 // calls it). `buf` holds one value per warp and NV; successive calls alternate between two buffers,
 // so one barrier per call is enough. The second stage reads the warps' sums four at a time.
-template <int NV> RSM_DEV void row_sum(float (&v)[NV], int tpr, float (*buf)[32]) {
+template <int THREADS, int NV> RSM_DEV void row_sum(float (&v)[NV], int tpr, float (*buf)[32]) {
+  if (THREADS <= 128 && tpr < 32) {
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+      for (int o = tpr >> 1; o > 0; o >>= 1) v[k] += __shfl_xor_sync(kFull, v[k], o);
+    return;
+  }
 #pragma unroll
   for (int k = 0; k < NV; ++k) v[k] = warp_sum_f(v[k]);
-  if (tpr == 32) return;
+  if (THREADS <= 128 && tpr == 32) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (lane == 0) {
 #pragma unroll
     for (int k = 0; k < NV; ++k) buf[k][warp] = v[k];
   }
   __syncthreads();
-  const int nw = tpr >> 5, w0 = warp & ~(nw - 1);  // (nw is a power of two, 2 to 16)
+  const int nw = tpr >> 5, w0 = nw < 4 ? warp & ~(nw - 1) : 0;  // (2, or a multiple of 4: then the row has the block)
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
     if (nw == 2) {
@@ -129,50 +141,113 @@ template <int GATE> RSM_DEV void activation(float2 g, float2& a, float2& slope) 
   }
 }
 
-// What a thread holds of a row. Rows behind the last one, and columns behind d, are zero.
-template <typename TY, typename T, int VEC, int ITER, bool GATED> struct Row {
-  Raw<TY, VEC> y[ITER];
-  Raw<T, VEC> g[ITER], r[ITER];
-  template <class A> RSM_DEV void load(const A& a, int64_t row, int t, int tpr) {
+// Rows come through a ring in shared memory that every warp fills, and reads, for itself: no barrier, no
+// registers for what is on its way, and a later pass reads again what an earlier one had. Lanes copy
+// neighbouring 16 bytes: where a thread's piece has 32 (8 fp32 values), as two copies of its own it would take
+// every sector twice (8 values of fp32 y with bf16 otherwise, 2^25 values: 89 us against 74).
+template <typename TX, int VEC, int ITER, int THREADS> struct Slot {
+  static constexpr int kPiece = VEC * (int)sizeof(TX), kChunk = kPiece < 16 ? kPiece : 16, kPer = kPiece / kChunk;
+  static constexpr int kBytes = ITER * kPiece * THREADS;
+  // Where chunk q of the warp's stands: pairs change places in every other group of eight, so that eight lanes
+  // which read every second chunk meet all banks.
+  static RSM_DEV int place(int i, int q) {
+    if (kPer == 2) q ^= (q >> 3) & 1;
+    return ((i * (THREADS / 32) + (int)(threadIdx.x >> 5)) * 32 * kPer + q) * kChunk;
+  }
+  // The thread's share of piece i of its warp's lanes in the row, of a row of d that starts at x + at; c is the
+  // thread's column.
+  static RSM_DEV void copy(unsigned char* slot, int i, const TX* x, int64_t at, int c, int d, bool there, int tpr) {
+    const int lane = threadIdx.x & 31, lanes = THREADS > 128 ? 32 : min(tpr, 32), l = lane & (lanes - 1);
 #pragma unroll
-    for (int i = 0; i < ITER; ++i) {
-      const int c = (t + i * tpr) * VEC;
-      y[i].zero(); g[i].zero(); r[i].zero();
-      if (row < a.rows && c < a.d) {
-        const int64_t at = row * a.d + c;
-        y[i].load(static_cast<const TY*>(a.y) + at);
-        if (GATED) g[i].load(static_cast<const T*>(a.gate) + at);
-        r[i].load(static_cast<const T*>(a.residual) + at);
-      }
+    for (int k = 0; k < kPer; ++k) {
+      const int q = lanes * k + l, col = c - l * VEC + q * (VEC / kPer);
+      const bool in = there && col < d;
+      const uint32_t to = (uint32_t)__cvta_generic_to_shared(slot + place(i, (lane - l) * kPer + q));
+      const TX* from = x + (in ? at + col : 0);
+      if constexpr (kChunk == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(in ? 16 : 0) : "memory");
+      else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to), "l"(from), "r"(in ? 8 : 0) : "memory");
     }
   }
-};
-template <typename T, int VEC, int ITER> struct Grads {
-  Raw<T, VEC> dx[ITER], dh[ITER];
-  template <class A> RSM_DEV void load(const A& a, int64_t row, int t, int tpr) {
+  static RSM_DEV Raw<TX, VEC> read(const unsigned char* slot, int i) {
+    Raw<TX, VEC> x;
+    constexpr int kWords = kChunk / 4;
 #pragma unroll
-    for (int i = 0; i < ITER; ++i) {
-      const int c = (t + i * tpr) * VEC;
-      dx[i].zero(); dh[i].zero();
-      if (row < a.rows && c < a.d) {
-        const int64_t at = row * a.d + c;
-        if (a.dx) dx[i].load(static_cast<const T*>(a.dx) + at);
-        if (a.dh) dh[i].load(static_cast<const T*>(a.dh) + at);
+    for (int k = 0; k < kPer; ++k) {
+      const unsigned char* at = slot + place(i, kPer * (threadIdx.x & 31) + k);
+      if constexpr (kChunk == 16) {
+        const uint4 t = *reinterpret_cast<const uint4*>(at);
+        x.w[kWords * k] = t.x; x.w[kWords * k + 1] = t.y; x.w[kWords * k + 2] = t.z; x.w[kWords * k + 3] = t.w;
+      } else {
+        const uint2 t = *reinterpret_cast<const uint2*>(at);
+        x.w[0] = t.x; x.w[1] = t.y;
       }
     }
+    return x;
   }
 };
 
-// The blocks stay and take row after row. Where a row is one piece per thread (ITER = 1) the next row is on
-// its way while this one is summed up and written: without that, the memory idles during the two row sums
-// (32768 rows of 2048, fp32 y: 236 us against 123 at the copy's rate).
+// y, gate, residual and, for the gradients, dx and dh of one row after the other.
+template <typename TY, typename T, int VEC, int ITER, int THREADS, bool BACK> struct Ring {
+  using Y = Slot<TY, VEC, ITER, THREADS>;
+  using X = Slot<T, VEC, ITER, THREADS>;
+  static constexpr int kTensors = BACK ? 5 : 3;
+  static constexpr int kStage = Y::kBytes + (kTensors - 1) * X::kBytes;
+  // Blocks per SM: as many threads as the registers of a thread's values, weights and sums leave room for.
+  static constexpr int kBlocks = (VEC * ITER <= 8 ? 768 : BACK ? 512 : 768) / THREADS;
+  static constexpr int kFit = (232448 / kBlocks - 2048) / kStage;
+  static constexpr int kStages = kFit < 2 ? 1 : 2;  // (three: bf16, 2^25 values, forward 64 us instead of 58, gradients 124 instead of 120)
+  static constexpr int kBytes = kStages * kStage;
+  static_assert(kBytes <= 232448 - 2048, "shared memory budget");
+  // Rows behind the last one, columns behind d, and what is not given are zeros.
+  template <class A> static RSM_DEV void fetch(unsigned char* ring, int stage, const A& a, int64_t row, int t, int tpr) {
+    unsigned char* to = ring + stage * kStage;
+    const bool there = row < a.rows;
+    const int64_t at = there ? row * a.d : 0;
+    __syncwarp();  // every lane has read its pieces of the stage
+#pragma unroll
+    for (int i = 0; i < ITER; ++i) {
+      const int c = (t + i * tpr) * VEC;
+      Y::copy(to, i, static_cast<const TY*>(a.y), at, c, a.d, there, tpr);
+      auto tensor = [&](int k, const void* x) {
+        X::copy(to + Y::kBytes + (k - 1) * X::kBytes, i, static_cast<const T*>(x ? x : a.residual), at, c, a.d, there && x, tpr);
+      };
+      if (a.gate) tensor(1, a.gate);
+      tensor(2, a.residual);
+      if constexpr (BACK) {
+        tensor(3, a.dx);
+        tensor(4, a.dh);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  // Every lane's part of the oldest stage is there.
+  static RSM_DEV void wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+    __syncwarp();
+  }
+  static RSM_DEV Raw<TY, VEC> y(const unsigned char* in, int i) { return Y::read(in, i); }
+  static RSM_DEV Raw<T, VEC> x(const unsigned char* in, int k, int i) { return X::read(in + Y::kBytes + (k - 1) * X::kBytes, i); }
+};
+constexpr int kGate = 1, kResidual = 2, kDx = 3, kDh = 4;  // of the ring
+
+// The blocks stay and take row after row; the next rows are on their way while this one is summed up and
+// written (without that, the memory idles during the two row sums: 32768 rows of 2048, fp32 y, 236 us against
+// 123 at the copy's rate).
 template <typename TY, typename T, int VEC, int ITER, int THREADS, int GATE>
-__global__ void __launch_bounds__(THREADS, ITER == 1 ? 768 / THREADS : 1) block_norm_kernel(const rsm_block_norm_args a, int tpr) {
+__global__ void __launch_bounds__(THREADS, Ring<TY, T, VEC, ITER, THREADS, false>::kBlocks)
+    block_norm_kernel(const rsm_block_norm_args a, int tpr) {
+  using R = Ring<TY, T, VEC, ITER, THREADS, false>;
   __shared__ __align__(16) float buf[2][32];
+  extern __shared__ __align__(16) unsigned char ring[];
   const int rpb = blockDim.x / tpr;
   const int t = threadIdx.x % tpr;
   const int64_t step = (int64_t)gridDim.x * rpb;
   const float inv_d = 1.f / (float)a.d;
+  int64_t row = (int64_t)blockIdx.x * rpb + threadIdx.x / tpr;
+#pragma unroll
+  for (int k = 0; k < R::kStages; ++k) R::fetch(ring, k, a, row + k * step, t, tpr);
   Raw<float, VEC> w1[ITER], w2[ITER];
 #pragma unroll
   for (int i = 0; i < ITER; ++i) {
@@ -183,45 +258,44 @@ __global__ void __launch_bounds__(THREADS, ITER == 1 ? 768 / THREADS : 1) block_
       if (a.w_pre) w2[i].load(a.w_pre + c);
     }
   }
-  Row<TY, T, VEC, ITER, GATE != kNoGate> next;
-  int64_t row = (int64_t)blockIdx.x * rpb + threadIdx.x / tpr;
-  if (ITER == 1) next.load(a, row, t, tpr);
+  int stage = 0;
   // (every thread of the block makes the same number of rounds: the sums hold barriers)
   for (int64_t row0 = (int64_t)blockIdx.x * rpb; row0 < a.rows; row0 += step, row += step) {
-    Row<TY, T, VEC, ITER, GATE != kNoGate> in;
-    if (ITER == 1) {
-      in = next;
-      next.load(a, row + step, t, tpr);
-    } else {
-      in.load(a, row, t, tpr);
-    }
+    R::wait();
+    const unsigned char* in = ring + stage * R::kStage;
     const bool live = row < a.rows;
     const int64_t base = row * a.d;
     float2 acc = both(0.f);
 #pragma unroll
-    for (int i = 0; i < ITER; ++i)
+    for (int i = 0; i < ITER; ++i) {
+      const Raw<TY, VEC> y = R::y(in, i);
 #pragma unroll
-      for (int j = 0; j < VEC / 2; ++j) acc = fma2(in.y[i][j], in.y[i][j], acc);
+      for (int j = 0; j < VEC / 2; ++j) acc = fma2(y[j], y[j], acc);
+    }
     float sum[1] = {acc.x + acc.y};
-    row_sum(sum, tpr, &buf[0]);
+    row_sum<THREADS>(sum, tpr, &buf[0]);
     const float2 r1 = both(a.scale * rsqrtf(sum[0] * inv_d + a.eps));
     acc = both(0.f);
     float2 h[ITER][VEC / 2];
 #pragma unroll
     for (int i = 0; i < ITER; ++i) {
       const int c = (t + i * tpr) * VEC;
+      const Raw<TY, VEC> y = R::y(in, i);
+      const Raw<T, VEC> r = R::x(in, kResidual, i), g = R::x(in, GATE == kNoGate ? kResidual : kGate, i);
 #pragma unroll
       for (int j = 0; j < VEC / 2; ++j) {
         float2 act, slope;
-        activation<GATE>(in.g[i][j], act, slope);
-        h[i][j] = fma2(mul2(mul2(in.y[i][j], r1), w1[i][j]), act, in.r[i][j]);
+        activation<GATE>(g[j], act, slope);
+        h[i][j] = fma2(mul2(mul2(y[j], r1), w1[i][j]), act, r[j]);
         acc = fma2(h[i][j], h[i][j], acc);
       }
       if (live && c < a.d) store_vec<T, VEC>(static_cast<T*>(a.h) + base + c, h[i]);
     }
+    R::fetch(ring, stage, a, row + R::kStages * step, t, tpr);
+    stage = stage + 1 == R::kStages ? 0 : stage + 1;
     if (a.w_pre) {
       sum[0] = acc.x + acc.y;
-      row_sum(sum, tpr, &buf[1]);
+      row_sum<THREADS>(sum, tpr, &buf[1]);
       const float2 r2 = both(rsqrtf(sum[0] * inv_d + a.eps));
 #pragma unroll
       for (int i = 0; i < ITER; ++i) {
@@ -234,17 +308,22 @@ __global__ void __launch_bounds__(THREADS, ITER == 1 ? 768 / THREADS : 1) block_
       __syncthreads();  // buf[0] is written again in the next round
     }
   }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 template <typename TY, typename T, int VEC, int ITER, int THREADS, int GATE>
-__global__ void __launch_bounds__(THREADS, 512 / THREADS)
+__global__ void __launch_bounds__(THREADS, Ring<TY, T, VEC, ITER, THREADS, true>::kBlocks)
     block_norm_backward_kernel(const rsm_block_norm_backward_args a, int tpr) {
+  using R = Ring<TY, T, VEC, ITER, THREADS, true>;
   __shared__ __align__(16) float buf[2][2][32];
-  extern __shared__ float sums[];  // [rpb][2][d]: joins the rows of a block, rpb > 1 only
+  extern __shared__ __align__(16) unsigned char ring[];
   const int rpb = blockDim.x / tpr;
   const int sub = threadIdx.x / tpr, t = threadIdx.x % tpr;
   const int64_t step = (int64_t)gridDim.x * rpb;
   const float inv_d = 1.f / (float)a.d;
+  int64_t row = (int64_t)blockIdx.x * rpb + sub;
+#pragma unroll
+  for (int k = 0; k < R::kStages; ++k) R::fetch(ring, k, a, row + k * step, t, tpr);
   Raw<float, VEC> w1[ITER], w2[ITER];
   float2 s1[ITER][VEC / 2], s2[ITER][VEC / 2];
 #pragma unroll
@@ -258,64 +337,56 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS)
       if (a.w_pre) w2[i].load(a.w_pre + c);
     }
   }
-  Row<TY, T, VEC, ITER, GATE != kNoGate> next;
-  Grads<T, VEC, ITER> next_d;
-  int64_t row = (int64_t)blockIdx.x * rpb + sub;
-  if (ITER == 1) {
-    next.load(a, row, t, tpr);
-    next_d.load(a, row, t, tpr);
-  }
+  int stage = 0;
   for (int64_t row0 = (int64_t)blockIdx.x * rpb; row0 < a.rows; row0 += step, row += step) {
-    Row<TY, T, VEC, ITER, GATE != kNoGate> in;
-    Grads<T, VEC, ITER> d;
-    if (ITER == 1) {
-      in = next;
-      d = next_d;
-      next.load(a, row + step, t, tpr);
-      next_d.load(a, row + step, t, tpr);
-    } else {
-      in.load(a, row, t, tpr);
-      d.load(a, row, t, tpr);
-    }
+    R::wait();
+    const unsigned char* in = ring + stage * R::kStage;
     const bool live = row < a.rows;
     const int64_t base = row * a.d;
     float2 acc = both(0.f);
 #pragma unroll
-    for (int i = 0; i < ITER; ++i)
+    for (int i = 0; i < ITER; ++i) {
+      const Raw<TY, VEC> y = R::y(in, i);
 #pragma unroll
-      for (int j = 0; j < VEC / 2; ++j) acc = fma2(in.y[i][j], in.y[i][j], acc);
+      for (int j = 0; j < VEC / 2; ++j) acc = fma2(y[j], y[j], acc);
+    }
     float one[1] = {acc.x + acc.y};
-    row_sum(one, tpr, &buf[0][0]);
+    row_sum<THREADS>(one, tpr, &buf[0][0]);
     const float rs1 = rsqrtf(one[0] * inv_d + a.eps);
     const float2 r1 = both(rs1), r1s = both(a.scale * rs1);
     float2 acc2 = acc = both(0.f);
     float2 h[ITER][VEC / 2];
 #pragma unroll
-    for (int i = 0; i < ITER; ++i)
+    for (int i = 0; i < ITER; ++i) {
+      const Raw<TY, VEC> y = R::y(in, i);
+      const Raw<T, VEC> r = R::x(in, kResidual, i), dx = R::x(in, kDx, i), g = R::x(in, GATE == kNoGate ? kResidual : kGate, i);
 #pragma unroll
       for (int j = 0; j < VEC / 2; ++j) {
         float2 act, slope;
-        activation<GATE>(in.g[i][j], act, slope);
-        h[i][j] = fma2(mul2(mul2(in.y[i][j], r1s), w1[i][j]), act, in.r[i][j]);
+        activation<GATE>(g[j], act, slope);
+        h[i][j] = fma2(mul2(mul2(y[j], r1s), w1[i][j]), act, r[j]);
         acc = fma2(h[i][j], h[i][j], acc);
-        acc2 = fma2(mul2(d.dx[i][j], w2[i][j]), h[i][j], acc2);
+        acc2 = fma2(mul2(dx[j], w2[i][j]), h[i][j], acc2);
       }
+    }
     float two[2] = {acc.x + acc.y, acc2.x + acc2.y};
-    row_sum(two, tpr, &buf[1][0]);
+    row_sum<THREADS>(two, tpr, &buf[1][0]);
     const float rs2 = rsqrtf(two[0] * inv_d + a.eps);
     const float2 r2 = both(rs2), k2 = both(-rs2 * rs2 * rs2 * (two[1] * inv_d)), al = both(a.scale);
     acc = both(0.f);
 #pragma unroll
     for (int i = 0; i < ITER; ++i) {
       const int c = (t + i * tpr) * VEC;
+      const Raw<TY, VEC> yy = R::y(in, i);
+      const Raw<T, VEC> dxx = R::x(in, kDx, i), dh = R::x(in, kDh, i), g = R::x(in, GATE == kNoGate ? kResidual : kGate, i);
       float2 dg[VEC / 2], dH[VEC / 2];
 #pragma unroll
       for (int j = 0; j < VEC / 2; ++j) {
         float2 act, slope;
-        activation<GATE>(in.g[i][j], act, slope);
-        const float2 dx = d.dx[i][j], y = in.y[i][j];
+        activation<GATE>(g[j], act, slope);
+        const float2 dx = dxx[j], y = yy[j];
         s2[i][j] = fma2(mul2(dx, h[i][j]), r2, s2[i][j]);
-        dH[j] = fma2(h[i][j], k2, fma2(mul2(dx, w2[i][j]), r2, d.dh[i][j]));
+        dH[j] = fma2(h[i][j], k2, fma2(mul2(dx, w2[i][j]), r2, dh[j]));
         const float2 du = mul2(dH[j], al), ya = mul2(y, r1), dn = mul2(du, act);
         if (GATE != kNoGate) dg[j] = mul2(mul2(du, slope), mul2(ya, w1[i][j]));
         s1[i][j] = fma2(dn, ya, s1[i][j]);
@@ -328,18 +399,22 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS)
       }
     }
     one[0] = acc.x + acc.y;
-    row_sum(one, tpr, &buf[0][1]);
+    row_sum<THREADS>(one, tpr, &buf[0][1]);
     const float2 k1 = both(-rs1 * rs1 * rs1 * (one[0] * inv_d));
     if (a.dy) {
 #pragma unroll
       for (int i = 0; i < ITER; ++i) {
         const int c = (t + i * tpr) * VEC;
+        const Raw<TY, VEC> y = R::y(in, i);
 #pragma unroll
-        for (int j = 0; j < VEC / 2; ++j) h[i][j] = fma2(in.y[i][j], k1, mul2(h[i][j], r1));
+        for (int j = 0; j < VEC / 2; ++j) h[i][j] = fma2(y[j], k1, mul2(h[i][j], r1));
         if (live && c < a.d) store_vec<TY, VEC>(static_cast<TY*>(a.dy) + base + c, h[i]);
       }
     }
+    R::fetch(ring, stage, a, row + R::kStages * step, t, tpr);
+    stage = stage + 1 == R::kStages ? 0 : stage + 1;
   }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
   float* part = static_cast<float*>(a.workspace) + (int64_t)blockIdx.x * 2 * a.d;
   if (rpb == 1) {
 #pragma unroll
@@ -352,6 +427,9 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS)
     }
     return;
   }
+  // the block's rows join where the ring was ([rpb][2][d], which is smaller)
+  float* sums = reinterpret_cast<float*>(ring);
+  __syncthreads();
 #pragma unroll
   for (int i = 0; i < ITER; ++i) {
     const int c = (t + i * tpr) * VEC;
@@ -386,68 +464,78 @@ __global__ void __launch_bounds__(256) weight_sum_kernel(const float* part, int 
   }
 }
 
-// Threads and values per thread for a row of d: pieces of `vec` values, the fewest threads (a power of two,
-// at least a warp) that hold the row in one piece each, at most 512.
+// Threads and values per thread for a row of d: pieces of `vec` values (16 bytes where the rows allow it), 8
+// values per thread up to 256 threads, then 16 up to 512 threads. (4, where a row has
+// 32 values or less and 8 lanes.) A row has a block of its own from 128 threads on: rows that share barriers wait for
+// one another (32768 rows of 1024, gradients: blocks of 256 threads 163 us, of 128 139).
 struct Shape {
   int vec, tpr, iter, threads;
 };
-Shape shape_of(int d, int vec) {
+Shape shape_for(int d, rsm_dtype dtype) {
   Shape s;
-  s.vec = vec;
-  const int pieces = d / s.vec;
-  s.tpr = 32;
-  while (s.tpr < pieces && s.tpr < kMaxThreads) s.tpr *= 2;
-  s.iter = (pieces + s.tpr - 1) / s.tpr;
-  s.iter = s.iter <= 2 ? s.iter : 4;
-  s.threads = std::max(s.tpr, 256);
+  s.vec = dtype == RSM_BF16 && d % 8 == 0 ? 8 : 4;
+  const int pieces = (d + s.vec - 1) / s.vec;
+  s.iter = pieces <= 8 ? 1 : (d <= 2048 ? 8 : 16) / s.vec;
+  const int per = (pieces + s.iter - 1) / s.iter;
+  s.tpr = per <= 8 ? 8 : per <= 16 ? 16 : per <= 32 ? 32 : per <= 64 ? 64 : (per + 127) / 128 * 128;
+  s.threads = std::max(s.tpr, 128);
   return s;
 }
-// 16-byte pieces where the rows allow it
-Shape shape_for(int d, rsm_dtype dtype) { return shape_of(d, dtype == RSM_BF16 && d % 8 == 0 ? 8 : 4); }
-int backward_blocks(int64_t rows, const Shape& s) {
+// Block size that the kernels are compiled for.
+int compiled_threads(const Shape& s) { return s.threads <= 128 ? 128 : s.threads <= 256 ? 256 : 512; }
+// As many blocks as stay resident, and no more than there are rows for.
+int blocks_for(int64_t rows, const Shape& s, int per_sm) {
   const int rpb = s.threads / s.tpr;
-  const int64_t need = (rows + rpb - 1) / rpb;
-  return (int)std::min<int64_t>(need, (int64_t)(512 / s.threads) * device_sm_count());
+  return (int)std::min<int64_t>((rows + rpb - 1) / rpb, (int64_t)per_sm * device_sm_count());
+}
+int backward_blocks(int64_t rows, const Shape& s) {
+  return blocks_for(rows, s, (s.vec * s.iter <= 8 ? 768 : 512) / compiled_threads(s));
 }
 
 template <class A> int gate_of(const A& a) { return !a.gate ? kNoGate : a.act == RSM_ACT_SILU ? kSilu : kSigmoid; }
 
-// Calls f with the block size and the gate as compile-time constants. (Rows of more than one piece per
-// thread always take the larger block.)
-template <int ITER, class F> void with_constants(int threads, int gate, F f) {
+// Calls f with the block size and the gate as compile-time constants.
+template <int VALUES, class F> cudaError_t with_constants(int threads, int gate, F f) {
   auto gated = [&](auto t) {
-    if (gate == kNoGate) f(t, std::integral_constant<int, kNoGate>());
-    else if (gate == kSilu) f(t, std::integral_constant<int, kSilu>());
-    else f(t, std::integral_constant<int, kSigmoid>());
+    if (gate == kNoGate) return f(t, std::integral_constant<int, kNoGate>());
+    if (gate == kSilu) return f(t, std::integral_constant<int, kSilu>());
+    return f(t, std::integral_constant<int, kSigmoid>());
   };
-  if constexpr (ITER == 1) {
+  if constexpr (VALUES <= 8) {
+    if (threads == 128) return gated(std::integral_constant<int, 128>());
+  }
+  if constexpr (VALUES >= 8) {
     if (threads == 256) return gated(std::integral_constant<int, 256>());
   }
-  gated(std::integral_constant<int, 512>());
+  if constexpr (VALUES == 16) {
+    if (threads == 512) return gated(std::integral_constant<int, 512>());
+  }
+  return cudaErrorInvalidConfiguration;
 }
 
 template <typename TY, typename T, int VEC, int ITER>
 cudaError_t forward_as(const rsm_block_norm_args& a, const Shape& s, cudaStream_t stream) {
-  const int rpb = s.threads / s.tpr;
-  const int64_t need = (a.rows + rpb - 1) / rpb;
-  const int64_t grid = std::min<int64_t>(need, (int64_t)(768 / s.threads) * device_sm_count());
-  with_constants<ITER>(s.threads, gate_of(a), [&](auto threads, auto gate) {
-    block_norm_kernel<TY, T, VEC, ITER, decltype(threads)::value, decltype(gate)::value>
-        <<<(unsigned)grid, s.threads, 0, stream>>>(a, s.tpr);
+  return with_constants<VEC * ITER>(compiled_threads(s), gate_of(a), [&](auto threads, auto gate) {
+    using R = Ring<TY, T, VEC, ITER, decltype(threads)::value, false>;
+    auto* kernel = block_norm_kernel<TY, T, VEC, ITER, decltype(threads)::value, decltype(gate)::value>;
+    cudaError_t e = set_smem_limit<block_norm_kernel<TY, T, VEC, ITER, decltype(threads)::value, decltype(gate)::value>>(R::kBytes);
+    if (e != cudaSuccess) return e;
+    kernel<<<(unsigned)blocks_for(a.rows, s, R::kBlocks), s.threads, R::kBytes, stream>>>(a, s.tpr);
+    return cudaGetLastError();
   });
-  return cudaGetLastError();
 }
 
 template <typename TY, typename T, int VEC, int ITER>
 cudaError_t backward_as(const rsm_block_norm_backward_args& a, const Shape& s, cudaStream_t stream) {
-  const int rpb = s.threads / s.tpr;
-  const int bytes = rpb > 1 ? rpb * 2 * a.d * 4 : 0;  // at most 8 * 2 * 256 * 4
   const int grid = backward_blocks(a.rows, s);
-  with_constants<ITER>(s.threads, gate_of(a), [&](auto threads, auto gate) {
-    block_norm_backward_kernel<TY, T, VEC, ITER, decltype(threads)::value, decltype(gate)::value>
-        <<<grid, s.threads, bytes, stream>>>(a, s.tpr);
+  cudaError_t e = with_constants<VEC * ITER>(compiled_threads(s), gate_of(a), [&](auto threads, auto gate) {
+    using R = Ring<TY, T, VEC, ITER, decltype(threads)::value, true>;
+    auto* kernel = block_norm_backward_kernel<TY, T, VEC, ITER, decltype(threads)::value, decltype(gate)::value>;
+    cudaError_t e = set_smem_limit<block_norm_backward_kernel<TY, T, VEC, ITER, decltype(threads)::value, decltype(gate)::value>>(R::kBytes);
+    if (e != cudaSuccess) return e;
+    kernel<<<grid, s.threads, R::kBytes, stream>>>(a, s.tpr);
+    return cudaGetLastError();
   });
-  cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !(a.dw_post || a.dw_pre)) return e;
   weight_sum_kernel<<<(2 * a.d + 31) / 32, 256, 0, stream>>>(static_cast<const float*>(a.workspace), grid, a.d,
                                                              a.dw_post, a.dw_pre);

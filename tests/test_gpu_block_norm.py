@@ -64,6 +64,37 @@ def test_forward_and_backward(rsm, rows, d, ty, t, act):
         close(n, v, want[n])
 
 
+@pytest.mark.parametrize("ty,t", [(F32, F32), (BF16, BF16), (F32, BF16)])
+@pytest.mark.parametrize("rows,d", [(37, 16), (1001, 12), (129, 60), (4000, 32), (130, 132), (33, 360), (700, 2500), (70, 1540),
+                                    (5, 6144), (300, 6148), (9, 5000)])
+def test_rows_that_share_a_warp_and_odd_widths(rsm, rows, d, ty, t):
+    """Rows of 8 and 16 lanes with a last block that is not full, and widths that leave lanes and pieces idle."""
+    test_forward_and_backward(rsm, rows, d, ty, t, "sigmoid")
+
+
+@pytest.mark.parametrize("ty,t", [(F32, F32), (BF16, BF16), (F32, BF16)])
+@pytest.mark.parametrize("rows,d", [(60000, 64), (20000, 100), (12000, 1024), (4000, 2500), (3000, 8192)])
+def test_in_place_over_many_rows(rsm, rows, d, ty, t):
+    """Blocks that read rows ahead of those they overwrite; and the gradients' bits do not change from call to call."""
+    x, dh, dx = inputs(rows, d, ty, t, seed=2)
+    want = rsm.block_norm_forward(**x)
+    first = rsm.block_norm_backward(**x, dh=dh, dx=dx)
+    again = rsm.block_norm_backward(**x, dh=dh, dx=dx)
+    assert all(torch.equal(first[n], again[n]) for n in first)
+    for name in ("residual", "y") if ty == t else ("residual",):
+        y = {n: v.clone() for n, v in x.items()}
+        r = rsm.block_norm_forward(**y, out={"h": y[name]})
+        assert torch.equal(r["h"], want["h"]) and torch.equal(r["x"], want["x"])
+    for part in (slice(0, 7), slice(rows - 7, rows)):
+        few = {n: (v if n.startswith("w_") else v[part].contiguous()) for n, v in x.items()}
+        w = hybrid.block_norm(few["y"], few["gate"], few["residual"], few["w_post"], few["w_pre"], "silu", 1.0, 1e-6,
+                              dh[part], dx[part])
+        for n in ("h", "x"):
+            close(n, want[n][part], w[n])
+        for n in ("dy", "dgate", "dresidual"):
+            close(n, first[n][part], w[n])
+
+
 @pytest.mark.parametrize("t", [BF16, F32])
 def test_optional_parts(rsm, t):
     x, dh, dx = inputs((2, 5), 96, t, t, seed=3)

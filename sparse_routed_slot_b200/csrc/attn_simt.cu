@@ -13,7 +13,9 @@
 // BB streamed ones: W = A B^T over the head dimension and acc += W B. Both read 16-byte pieces of
 // shared memory, the rows padded by 16 bytes so that 8 neighbouring rows use different banks. What bounds
 // them is shared memory, which hands out 32 words a cycle: a thread's 4 x 4 (4 x 2) products use a word
-// twice (1.3 times) and the FMA pipe could take 4. Neither 8 rows per thread and half the threads nor warp-level
+// twice (1.3 times) and the FMA pipe could take 4. A score is four interleaved sums, two per packed FMA: as one
+// sum of D terms it is off by twice as much, and o, dq and dk with it (2 x 777 tokens: 5.8e-7 of the gradients'
+// norm, now 3.9e-7; the same time). Neither 8 rows per thread and half the threads nor warp-level
 // tf32 products of split operands were faster at the sizes fp32 runs at, where blocks are few and latency
 // counts (forward and gradients of 2 x 777 tokens, 4 heads of 64: 234 and 201 us a call against 175).
 #include <algorithm>
@@ -83,11 +85,12 @@ RSM_DEV void load_rows(float* dst, const void* base, int D, int tx, int ty, Off 
 // c[i][j] = sum_d A[ty + 16 i][d] B[tx + 16 j][d]
 template <int DP, int BB>
 RSM_DEV void product_nt(const float* A, const float* B, int D, int tx, int ty, float (&c)[4][BB / 16]) {
+  float2 s[4][BB / 16][2];  // four sums per score, joined at the end: one sum of D terms is off by twice as much
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int j = 0; j < BB / 16; ++j) c[i][j] = 0.f;
-#pragma unroll 4
+    for (int j = 0; j < BB / 16; ++j) s[i][j][0] = s[i][j][1] = both(0.f);
+#pragma unroll 2
   for (int d = 0; d < D; d += 4) {
     float4 a[4], b[BB / 16];
 #pragma unroll
@@ -98,12 +101,14 @@ RSM_DEV void product_nt(const float* A, const float* B, int D, int tx, int ty, f
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int j = 0; j < BB / 16; ++j) {
-        c[i][j] = fmaf(a[i].x, b[j].x, c[i][j]);
-        c[i][j] = fmaf(a[i].y, b[j].y, c[i][j]);
-        c[i][j] = fmaf(a[i].z, b[j].z, c[i][j]);
-        c[i][j] = fmaf(a[i].w, b[j].w, c[i][j]);
+        s[i][j][0] = fma2(make_float2(a[i].x, a[i].y), make_float2(b[j].x, b[j].y), s[i][j][0]);
+        s[i][j][1] = fma2(make_float2(a[i].z, a[i].w), make_float2(b[j].z, b[j].w), s[i][j][1]);
       }
   }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < BB / 16; ++j) c[i][j] = (s[i][j][0].x + s[i][j][0].y) + (s[i][j][1].x + s[i][j][1].y);
 }
 
 // acc[i][jj] += sum_k W[ty + 16 i][k] B[k][4 tx + 64 jj ..]
@@ -122,10 +127,9 @@ RSM_DEV void product_nn(const float* W, const float* B, int tx, int ty, float4 (
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float x = u == 0 ? w[i].x : u == 1 ? w[i].y : u == 2 ? w[i].z : w[i].w;
-          acc[i][jj].x = fmaf(x, b.x, acc[i][jj].x);
-          acc[i][jj].y = fmaf(x, b.y, acc[i][jj].y);
-          acc[i][jj].z = fmaf(x, b.z, acc[i][jj].z);
-          acc[i][jj].w = fmaf(x, b.w, acc[i][jj].w);
+          const float2 lo = fma2(both(x), make_float2(b.x, b.y), make_float2(acc[i][jj].x, acc[i][jj].y));
+          const float2 hi = fma2(both(x), make_float2(b.z, b.w), make_float2(acc[i][jj].z, acc[i][jj].w));
+          acc[i][jj] = make_float4(lo.x, lo.y, hi.x, hi.y);
         }
       }
     }
@@ -201,17 +205,17 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const AttnParams p,
       for (int j = 0; j < BB / 16; ++j) {
         const int key = k0 + tx + 16 * j;
         const bool seen = used[tx + 16 * j] && sees(pos[i], key, p.window, p.sinks);
-        c[i][j] = seen ? c[i][j] * scale2 : kNegInf;
+        if (!seen) c[i][j] = kNegInf;
         top = fmaxf(top, c[i][j]);
       }
       const float mn = fmaxf(m[i], half_warp_max(top));
       const float ref = mn == kNegInf ? 0.f : mn;  // nothing seen yet: every weight below is e^-inf = 0
-      const float corr = exp2f(m[i] - ref);
+      const float corr = exp2f((m[i] - ref) * scale2);  // (m is in the products' units: a difference rounds less)
       m[i] = mn;
       float sum = 0.f;
 #pragma unroll
       for (int j = 0; j < BB / 16; ++j) {
-        const float x = exp2f(c[i][j] - ref);
+        const float x = exp2f((c[i][j] - ref) * scale2);
         sum += x;
         sP[(ty + 16 * i) * (BB + 4) + tx + 16 * j] = x;
       }
@@ -231,7 +235,7 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const AttnParams p,
     if (r >= rows) continue;
     const int64_t at = q_index(r);
     const float inv = l[i] > 0.f ? 1.f / l[i] : l[i] == 0.f ? 0.f : l[i];  // (a NaN stays one)
-    const float lse = l[i] == 0.f ? kNegInf : (m[i] + log2f(l[i])) * kLn2;
+    const float lse = l[i] == 0.f ? kNegInf : fmaf(m[i], p.scale, logf(l[i]));
 #pragma unroll
     for (int jj = 0; jj < DP / 64; ++jj) {
       const int d = 4 * tx + 64 * jj;
@@ -275,7 +279,7 @@ __global__ void __launch_bounds__(kThreads) attn_simt_backward_kernel(const Attn
   float* sB2 = sB1 + BB * (DP + 4);
   float* sW2 = sB2 + BB * (DP + 4);
   float* sW1 = sW2 + kBA * (BB + 4);              // DQ: not used
-  float* sStat = DQ ? sW1 : sW1 + kBA * (BB + 4);  // lse (base 2) and delta of the query rows
+  float* sStat = DQ ? sW1 : sW1 + kBA * (BB + 4);  // lse and delta of the query rows
   int tile, pair, part = 0;
   if (DQ) {
     tile = blockIdx.x % ntiles;
@@ -300,7 +304,7 @@ __global__ void __launch_bounds__(kThreads) attn_simt_backward_kernel(const Attn
   auto load_stats = [&](int r0, int n) {
     for (int r = threadIdx.x; r < n; r += kThreads) {
       const bool in = r0 + r < nrows;
-      sStat[2 * r] = in ? p.lse[q_index(r0 + r)] * kLog2e : 0.f;
+      sStat[2 * r] = in ? p.lse[q_index(r0 + r)] : 0.f;
       sStat[2 * r + 1] = in ? p.delta[q_index(r0 + r)] : 0.f;
     }
   };
@@ -326,7 +330,6 @@ __global__ void __launch_bounds__(kThreads) attn_simt_backward_kernel(const Attn
       w1 = (int)((int64_t)walk.n * (part + 1) / cut.parts);
     }
   }
-  const float scale2 = p.scale * kLog2e;
   int pos[4];  // DQ: the rows' places
 #pragma unroll
   for (int i = 0; i < 4; ++i) pos[i] = (a0 + ty + 16 * i) / G;
@@ -364,7 +367,7 @@ __global__ void __launch_bounds__(kThreads) attn_simt_backward_kernel(const Attn
         const bool in_a = DQ ? a0 + ra < nrows : a0 + ra < T_;
         const float* st = sStat + 2 * (DQ ? ra : rb);
         const bool seen = there && in_a && (DQ ? sees(pos[i], b0 + rb, p.window, p.sinks) : sees(pos_b, a0 + ra, p.window, p.sinks));
-        const float pr = seen ? exp2f(c1[i][j] * scale2 - st[0]) : 0.f;
+        const float pr = seen ? exp2f(fmaf(c1[i][j], p.scale, -st[0]) * kLog2e) : 0.f;
         const float ds = seen ? pr * (c2[i][j] - st[1]) : 0.f;
         sW2[ra * (BB + 4) + rb] = ds;
         if (!DQ) sW1[ra * (BB + 4) + rb] = pr;

@@ -2,9 +2,11 @@
 // key/value head and sequence), bf16.
 //
 // Such a call reads every key and value once and computes little: it is bound by that read. Each warp walks
-// its own tiles of 16 keys (every eighth of the block's) through a ring in shared memory that it fills by
-// asynchronous copies, 16 bytes per lane, two tiles ahead: 8 warps keep 128 KB in flight (head dimension 128),
-// and no warp waits for another until the end. (Straight to registers, 16 warps with a tile each got 4.0 TB/s,
+// its own tiles of 16 keys (every fourth of the block's) through a ring in shared memory that it fills by
+// asynchronous copies, 16 bytes per lane, two tiles ahead: the 8 warps of an SM keep 128 KB in flight (head
+// dimension 128), and no warp waits for another until the end. An SM has two blocks, so that one's start and
+// join hide behind the other's reads (one block of 8 warps: 128 sequences of 2048 keys, 4/4 heads of 128, 116 us
+// against 106, of 100 keys, heads of 64, 32 against 19). (Straight to registers, 16 warps with a tile each got 4.0 TB/s,
 // 8 warps with two tiles 3.7.) The rest are warp-level tensor products (m16n8k16) with Q's rows as the narrow
 // side, so that none of it is wasted on up to 8 query rows:
 //   S^T = K Q^T   16 keys x 8 rows. A product sums over columns in any order, so lane 4 g + t takes the
@@ -68,7 +70,7 @@ RSM_DEV float over_keys_sum(float v) {
 }
 
 template <int DP> struct Layout {
-  static constexpr int kWarps = DP <= 128 ? 8 : 4, kThreads = 32 * kWarps;
+  static constexpr int kWarps = DP <= 128 ? 4 : 2, kThreads = 32 * kWarps;
   static constexpr int kTile = kKeys * DP * 2;            // bytes of a tile of keys (or values)
   static constexpr int kStages = DP <= 64 ? 6 : 3;        // 192 KB in all
   static constexpr int kBytes = kWarps * kStages * 2 * kTile;
@@ -86,7 +88,7 @@ RSM_DEV uint4 lds16(uint32_t at) {
 
 // NQ: groups of 8 query rows. A row is (token, head of the group), as everywhere.
 template <int DP, int NQ>
-__global__ void __launch_bounds__(Layout<DP>::kThreads, 1) attn_decode_kernel(const AttnParams p) {
+__global__ void __launch_bounds__(Layout<DP>::kThreads, 2) attn_decode_kernel(const AttnParams p) {
   using L = Layout<DP>;
   constexpr int kWarps = L::kWarps, kThreads = L::kThreads, kStages = L::kStages;
   constexpr int kR = 8 * NQ;

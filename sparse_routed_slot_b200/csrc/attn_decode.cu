@@ -86,8 +86,11 @@ RSM_DEV uint4 lds16(uint32_t at) {
   return x;
 }
 
-// NQ: groups of 8 query rows. A row is (token, head of the group), as everywhere.
-template <int DP, int NQ>
+// NQ: groups of 8 query rows. A row is (token, head of the group), as everywhere. ONE: a tile of keys stands in
+// one page (pages of multiples of 16); else each half does (multiples of 8), or rows are looked up one by one.
+// (40 sequences of 5000 keys, pages of 24: row by row 110 us, by halves 57; two starts per tile where one does
+// cost 2 to 3 %.)
+template <int DP, int NQ, bool ONE>
 __global__ void __launch_bounds__(Layout<DP>::kThreads, 2) attn_decode_kernel(const AttnParams p) {
   using L = Layout<DP>;
   constexpr int kWarps = L::kWarps, kThreads = L::kThreads, kStages = L::kStages;
@@ -125,7 +128,7 @@ __global__ void __launch_bounds__(Layout<DP>::kThreads, 2) attn_decode_kernel(co
   const int w0 = (int)((int64_t)walk.n * split / p.splits), w1 = (int)((int64_t)walk.n * (split + 1) / p.splits);
   const float scale2 = p.scale * kLog2e;
   const int64_t row_step = (int64_t)p.Hkv * D;
-  const bool one_page = p.page % kKeys == 0;  // a tile of keys stands in one page
+  const bool known = ONE || p.page % 8 == 0;  // where a tile's halves start is looked up ahead
   float m[NQ][2], l[NQ][2], o[NQ][kB * 4][4];
   int pos[NQ][2];  // places of rows 8 n + 2 t and + 1
 #pragma unroll
@@ -137,33 +140,49 @@ __global__ void __launch_bounds__(Layout<DP>::kThreads, 2) attn_decode_kernel(co
 #pragma unroll
     for (int j = 0; j < kB * 4; ++j) o[n][j][0] = o[n][j][1] = o[n][j][2] = o[n][j][3] = 0.f;
   }
-  // Offset of key k0 + i of a tile; -1 where there is no such key. `base` is that of k0 where one page has all.
-  auto offset = [&](int k0, int i, int64_t base) -> int64_t {
+  // Where a tile of keys, or each half of it, starts; -1 where there is no such key or page.
+  struct Base {
+    int64_t part[ONE ? 1 : 2];
+  };
+  // Offset of key k0 + i of a tile; -1 where there is no such key.
+  auto offset = [&](int k0, int i, const Base& base) -> int64_t {
     if (k0 + i >= s.kv) return -1;
-    return one_page ? (base < 0 ? -1 : base + i * row_step) : kv_offset(p, b, hk, k0 + i);
+    if (!known) return kv_offset(p, b, hk, k0 + i);
+    const int64_t from = base.part[ONE || i < 8 ? 0 : 1];
+    return from < 0 ? -1 : from + (ONE ? i : i & 7) * row_step;
   };
-  auto tile_base = [&](int w) -> int64_t {
-    return one_page && w < w1 ? kv_offset(p, b, hk, walk.tile(w) * kKeys) : -1;
+  auto tile_base = [&](int w) {
+    Base base;
+    const int k0 = w < w1 ? walk.tile(w) * kKeys : 0;
+#pragma unroll
+    for (int h = 0; h < (ONE ? 1 : 2); ++h)
+      base.part[h] = known && w < w1 && k0 + 8 * h < s.kv ? kv_offset(p, b, hk, k0 + 8 * h) : -1;
+    return base;
   };
+  auto held = [&](const Base& base) { return base.part[0] >= 0 && (ONE || base.part[ONE ? 0 : 1] >= 0); };
   const uint32_t ring = (uint32_t)__cvta_generic_to_shared(sm) + warp * (kStages * 2 * L::kTile);
   // Pieces stand in an order of their own per row, so that the 8 lanes of a quarter warp read different banks:
   // lanes g = 2 i, 2 i + 1 and all t of the keys, lanes g = 2 i, 2 i + 1 and rows 2 t of the values.
   auto k_at = [](int row, int piece) { return (uint32_t)(row * DP * 2 + ((piece ^ ((row & 1) << 2)) << 4)); };
   auto v_at = [](int row, int piece) { return (uint32_t)(row * DP * 2 + ((piece ^ (row & 6)) << 4)); };
-  // Nearly every tile is a whole one of one page: its addresses are a lane's place plus multiples of a row, its
+  // Nearly every tile is a whole one of known pages: its addresses are a lane's place plus multiples of a row, its
   // scores are all seen. (With the general arithmetic for every tile, 780 instructions per tile and warp, the
   // arithmetic and not the memory set the pace: 434 us for the step of 256.)
-  const bool full_rows = one_page && D == DP;
+  const bool full_rows = known && D == DP;
   const __nv_bfloat16* lane_k = static_cast<const __nv_bfloat16*>(p.k) + (lane / kPieces) * row_step + 8 * (lane % kPieces);
   const __nv_bfloat16* lane_v = static_cast<const __nv_bfloat16*>(p.v) + (lane / kPieces) * row_step + 8 * (lane % kPieces);
   const int64_t hop = (32 / kPieces) * row_step;  // from one copy of the lane to its next
-  auto fetch = [&](int w, int64_t base, int stage) {
+  auto fetch = [&](int w, const Base& base, int stage) {
     const uint32_t to = ring + stage * 2 * L::kTile;
     const int k0 = walk.tile(w) * kKeys;
-    if (full_rows && w < w1 && base >= 0 && k0 + kKeys <= s.kv) {
-      const __nv_bfloat16 *fk = lane_k + base, *fv = lane_v + base;
+    if (full_rows && w < w1 && held(base) && k0 + kKeys <= s.kv) {
+      const __nv_bfloat16 *fk = lane_k + base.part[0], *fv = lane_v + base.part[0];
 #pragma unroll
       for (int i = 0; i < kKeys * kPieces / 32; ++i) {
+        if (!ONE && i == kKeys * kPieces / 64) {
+          fk = lane_k + base.part[ONE ? 0 : 1];
+          fv = lane_v + base.part[ONE ? 0 : 1];
+        }
         const int row = 32 / kPieces * i + lane / kPieces;
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + k_at(row, lane % kPieces)), "l"(fk) : "memory");
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + L::kTile + v_at(row, lane % kPieces)), "l"(fv)
@@ -185,10 +204,10 @@ __global__ void __launch_bounds__(Layout<DP>::kThreads, 2) attn_decode_kernel(co
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  auto attend = [&](int w, int64_t base, int stage) {
+  auto attend = [&](int w, const Base& base, int stage) {
     const int k0 = walk.tile(w) * kKeys;
     const uint32_t from = ring + stage * 2 * L::kTile;
-    const bool whole = one_page && base >= 0 && k0 + kKeys <= s.kv && k0 + kKeys - 1 <= s.pos0 &&
+    const bool whole = known && held(base) && k0 + kKeys <= s.kv && k0 + kKeys - 1 <= s.pos0 &&
                        (p.window <= 0 || s.pos0 + nq - 1 - k0 < p.window || k0 + kKeys <= p.sinks);
     uint4 k[2][kC];
 #pragma unroll
@@ -255,7 +274,7 @@ __global__ void __launch_bounds__(Layout<DP>::kThreads, 2) attn_decode_kernel(co
   };
   {
     // `base` of the tiles in the ring and of the one after them: the table's answer comes a step ahead of its use
-    int64_t bases[kStages];
+    Base bases[kStages];
 #pragma unroll
     for (int i = 0; i < kStages; ++i) bases[i] = tile_base(w0 + warp + i * kWarps);
 #pragma unroll
@@ -264,7 +283,7 @@ __global__ void __launch_bounds__(Layout<DP>::kThreads, 2) attn_decode_kernel(co
 #pragma unroll 1
     for (int w = w0 + warp; w < w1; w += kWarps) {
       fetch(w + (kStages - 1) * kWarps, bases[kStages - 1], stage == 0 ? kStages - 1 : stage - 1);
-      const int64_t coming = tile_base(w + kStages * kWarps);
+      const Base coming = tile_base(w + kStages * kWarps);
       asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
       __syncwarp();  // every lane's part of the tile
       attend(w, bases[0], stage);
@@ -359,15 +378,15 @@ __global__ void __launch_bounds__(Layout<DP>::kThreads, 2) attn_decode_kernel(co
   cluster.sync();  // no block leaves while another reads its memory
 }
 
-template <int DP, int NQ> cudaError_t launch_as(const AttnParams& p, cudaStream_t stream) {
+template <int DP, int NQ, bool ONE> cudaError_t launch_as(const AttnParams& p, cudaStream_t stream) {
   constexpr int bytes = Layout<DP>::kBytes;
   static_assert(bytes <= 232448 - 4096, "shared memory budget");
-  cudaError_t e = set_smem_limit<attn_decode_kernel<DP, NQ>>(bytes);
+  cudaError_t e = set_smem_limit<attn_decode_kernel<DP, NQ, ONE>>(bytes);
   if (e != cudaSuccess) return e;
   const int64_t grid = (int64_t)p.B * p.Hkv * p.splits;
   if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
   if (p.splits == 1 || p.splits > kCluster) {
-    attn_decode_kernel<DP, NQ><<<(unsigned)grid, Layout<DP>::kThreads, bytes, stream>>>(p);
+    attn_decode_kernel<DP, NQ, ONE><<<(unsigned)grid, Layout<DP>::kThreads, bytes, stream>>>(p);
     return cudaGetLastError();
   }
   cudaLaunchConfig_t config = {};
@@ -381,7 +400,7 @@ template <int DP, int NQ> cudaError_t launch_as(const AttnParams& p, cudaStream_
   cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
   config.attrs = &cluster;
   config.numAttrs = 1;
-  return cudaLaunchKernelEx(&config, attn_decode_kernel<DP, NQ>, p);
+  return cudaLaunchKernelEx(&config, attn_decode_kernel<DP, NQ, ONE>, p);
 }
 
 }  // namespace
@@ -391,22 +410,26 @@ bool attn_decode_supported(const AttnParams& p, rsm_dtype dtype) {
   return dtype == RSM_BF16 && p.table && p.num_pages > 0 && p.table_width > 0 && (int64_t)p.max_q * p.G <= 16;
 }
 
-// Blocks that share a sequence's keys: where sequences and heads alone are fewer than four blocks per SM,
-// enough for that, of at least 128 keys each (one tile per warp) by the table's width.
+// Blocks that share a sequence's keys: where sequences and heads alone are fewer blocks than stay resident (two
+// per SM), enough for that, of at least 128 keys each by the table's width. (Twice as many: 40 sequences of
+// 5000 keys, 2 heads of 80, 79 us against 54; 32 of 2048, 4 heads of 128, 49 against 42.)
 int attn_decode_splits(const AttnParams& p) {
   int64_t keys = (int64_t)p.table_width * p.page;
   if (p.window > 0) keys = std::min<int64_t>(keys, (int64_t)p.window + p.sinks + p.max_q);
-  const int64_t want = 4 * device_sm_count() / std::max<int64_t>(1, (int64_t)p.B * p.Hkv);
+  const int64_t want = 2 * device_sm_count() / std::max<int64_t>(1, (int64_t)p.B * p.Hkv);
   return (int)std::max<int64_t>(1, std::min<int64_t>({want, keys / (kKeys * 8), 64}));
 }
 
 bool attn_decode_joins(const AttnParams& p) { return p.splits <= kCluster; }
 
+template <int DP> cudaError_t launch_rows(const AttnParams& p, cudaStream_t stream) {
+  const bool two = p.max_q * p.G > 8, one = p.page % kKeys == 0;
+  if (two) return one ? launch_as<DP, 2, true>(p, stream) : launch_as<DP, 2, false>(p, stream);
+  return one ? launch_as<DP, 1, true>(p, stream) : launch_as<DP, 1, false>(p, stream);
+}
+
 cudaError_t launch_attn_decode(const AttnParams& p, cudaStream_t stream) {
-  const bool two = p.max_q * p.G > 8;
-  if (p.D <= 64) return two ? launch_as<64, 2>(p, stream) : launch_as<64, 1>(p, stream);
-  if (p.D <= 128) return two ? launch_as<128, 2>(p, stream) : launch_as<128, 1>(p, stream);
-  return two ? launch_as<256, 2>(p, stream) : launch_as<256, 1>(p, stream);
+  return p.D <= 64 ? launch_rows<64>(p, stream) : p.D <= 128 ? launch_rows<128>(p, stream) : launch_rows<256>(p, stream);
 }
 
 }  // namespace rsm

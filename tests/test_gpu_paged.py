@@ -236,6 +236,32 @@ def test_caches_without_pages(rsm, dtype, new, pages, width):
         assert not r["o"].any() and (r["lse"] == float("-inf")).all() and not kc.any()
 
 
+@pytest.mark.parametrize("page", [8, 24, 40, 16, 12])
+@pytest.mark.parametrize("H,Hkv,D,new", [(4, 1, 128, 1), (8, 2, 64, 4), (6, 2, 80, 3), (4, 1, 256, 4), (5, 5, 128, 1)])
+def test_few_rows_by_page_size(rsm, page, H, Hkv, D, new):
+    """Tiles of 16 keys in one page, in two, and row by row; lengths around tiles, halves and pages."""
+    for lens in ([5, 8, 9, 16], [17, 23, 24, 25], [40, 47, 48, 200], [1000, 39, 41, 7]):
+        c = Cache([new] * 4, lens, H, Hkv, D, page, BF16, seed=page + D)
+        c.check(rsm)
+        c.check(rsm, W=20, S=3)
+
+
+@pytest.mark.parametrize("page,slot", [(8, 2), (8, 3), (24, 1), (40, 0), (16, 1)])
+def test_few_rows_with_a_page_missing(rsm, page, slot):
+    """A tile of which only one half has its page."""
+    c = Cache([1, 1], [130, 77], 8, 2, 128, page, BF16, seed=page + slot)
+    c.append(rsm)
+    c.table[0, slot] = -1
+    r = rsm.paged_forward(c.q, *c.args(), 1)
+    assert rsm.device_status() == 7 and rsm.device_status() == 0
+    keep = [j for j in range(130) if j // page != slot]
+    u, uo = roundings(BF16)
+    for b, kept in ((0, keep), (1, list(range(77)))):
+        w = hybrid.attend(c.q[b:b + 1], c.keys[b][kept], c.values[b][kept], torch.tensor([len(kept) - 1], device="cuda"), 0, 0,
+                          1 / math.sqrt(128), None, u, uo)
+        within("o", r["o"][b:b + 1], *w["o"])
+
+
 def test_far_pages(rsm):
     """A cache whose last page lies past 2^31 elements and 2^32 bytes."""
     Hkv, D, page = 8, 128, 64

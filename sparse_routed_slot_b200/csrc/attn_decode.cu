@@ -5,7 +5,7 @@
 // its own tiles of 16 keys (every fourth of the block's) through a ring in shared memory that it fills by
 // asynchronous copies, 16 bytes per lane, two tiles ahead: the 8 warps of an SM keep 128 KB in flight (head
 // dimension 128), and no warp waits for another until the end. An SM has two blocks, so that one's start and
-// join hide behind the other's reads (one block of 8 warps: 128 sequences of 2048 keys, 4/4 heads of 128, 116 us
+// join hide behind the other's reads (one block of 8 warps: 128 sequences of 2048 keys, 16/4 heads of 128, 116 us
 // against 106, of 100 keys, heads of 64, 32 against 19). (Straight to registers, 16 warps with a tile each got 4.0 TB/s,
 // 8 warps with two tiles 3.7.) The rest are warp-level tensor products (m16n8k16) with Q's rows as the narrow
 // side, so that none of it is wasted on up to 8 query rows:
@@ -167,7 +167,8 @@ __global__ void __launch_bounds__(Layout<DP>::kThreads, 2) attn_decode_kernel(co
   auto v_at = [](int row, int piece) { return (uint32_t)(row * DP * 2 + ((piece ^ (row & 6)) << 4)); };
   // Nearly every tile is a whole one of known pages: its addresses are a lane's place plus multiples of a row, its
   // scores are all seen. (With the general arithmetic for every tile, 780 instructions per tile and warp, the
-  // arithmetic and not the memory set the pace: 434 us for the step of 256.)
+  // arithmetic and not the memory set the pace: 434 us for 256 sequences of 2048 to 4096 keys, 16/4 heads of 128,
+  // which take 268 to 282 now.)
   const bool full_rows = known && D == DP;
   const __nv_bfloat16* lane_k = static_cast<const __nv_bfloat16*>(p.k) + (lane / kPieces) * row_step + 8 * (lane % kPieces);
   const __nv_bfloat16* lane_v = static_cast<const __nv_bfloat16*>(p.v) + (lane / kPieces) * row_step + 8 * (lane % kPieces);
@@ -412,7 +413,7 @@ bool attn_decode_supported(const AttnParams& p, rsm_dtype dtype) {
 
 // Blocks that share a sequence's keys: where sequences and heads alone are fewer blocks than stay resident (two
 // per SM), enough for that, of at least 128 keys each by the table's width. (Twice as many: 40 sequences of
-// 5000 keys, 2 heads of 80, 79 us against 54; 32 of 2048, 4 heads of 128, 49 against 42.)
+// 5000 keys, 8/2 heads of 80, 79 us against 54; 32 of 2048, 16/4 heads of 128, 49 against 42.)
 int attn_decode_splits(const AttnParams& p) {
   int64_t keys = (int64_t)p.table_width * p.page;
   if (p.window > 0) keys = std::min<int64_t>(keys, (int64_t)p.window + p.sinks + p.max_q);

@@ -279,7 +279,8 @@ rsm_status rsm_window_backward(const rsm_window_backward_args* a, void* stream) 
   } else if (e == cudaSuccess) {
     p.delta = static_cast<float*>(a->workspace);
     e = rsm::launch_attn_delta(p, a->dtype, st);
-    if (e == cudaSuccess) e = rsm::launch_attn_simt_backward(p, a->dtype, reinterpret_cast<float*>(static_cast<char*>(a->workspace) + delta_bytes(*a)), st);
+    float* parts = reinterpret_cast<float*>(static_cast<char*>(a->workspace) + delta_bytes(*a));
+    if (e == cudaSuccess) e = rsm::launch_attn_simt_backward(p, a->dtype, parts, st);
   }
   return finish(e, "rsm_window_backward");
 }

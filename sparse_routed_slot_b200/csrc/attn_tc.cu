@@ -96,8 +96,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
   constexpr int NS = L::kStages;
   constexpr int kBlocks = DP / 64;  // 64-column blocks of a tile
   extern __shared__ unsigned char smem_raw[];
-  __shared__ uint64_t q_full[2], full[NS], empty[NS], s_full[2][2], p_full[2][2],
-      fin[2];
+  __shared__ uint64_t q_full[2], full[NS], empty[NS], s_full[2][2], p_full[2][2], o_done[2], fin[2];
   __shared__ uint32_t bad_keys[NS];
   __shared__ uint32_t s_tbase;
 
@@ -128,6 +127,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         tc::mbar_init(&s_full[i][u], 1);
         tc::mbar_init(&p_full[i][u], 4);
       }
+      tc::mbar_init(&o_done[i], 1);
       tc::mbar_init(&fin[i], 1);
     }
     for (int i = 0; i < NS; ++i) {
@@ -238,6 +238,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
 #pragma unroll
           for (int j = 0; j < kBN / 16; ++j)
             tc::mma_bf16_ts(cO, cS + (np & 1) * kBN + 8 * j, v + (uint64_t)(j * 2048 >> 4), kIdO, np > 0 || j > 0);
+          tc::mma_commit(&o_done[t]);
           ++np;
         }
         if (c < n && act(c)) {
@@ -275,7 +276,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                                  s.kv, p, t || ntiles > 1);
     const int theirs = other.count();
     const int my_turn = 1 + 2 * (warp & 3) + t, their_turn = 1 + 2 * (warp & 3) + 1 - t;
-    int last = 0;  // the step before this one
     // Scores of step i into x (hidden ones -inf), and the row's reference moved where it has to. False: a wait expired.
     auto look = [&](int i, int k0, bool there, uint32_t tP, float (&x)[kBN]) {
       if (!there && !wait_warp(&s_full[t][done & 1], (done >> 1) & 1)) return false;
@@ -330,9 +330,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       const bool move = done == 0 || top > m + kSlack;
       // (a row that has seen nothing yet has nothing to rescale)
       if (__any_sync(kFull, move && m != kNegInf)) {
-        // O is this warp's once the last product into it is done, that is once its unit is let go of. (The
-        // unit that takes the stage next comes behind this tile's product, so the parity names one phase.)
-        if (!wait_warp(&empty[(last + 2) % NS], ((last + 2) / NS) & 1)) return false;
+        // O is this warp's once the last product into it is done. (The next one takes this warp's weights, so
+        // the parity names one phase.) Not once that product's unit is let go of, which takes the other tile's
+        // issuer as well: with one query head per key/value head the other tile can be two steps ahead, and its
+        // rows wait for the turn that this warp holds.
+        if (!wait_warp(&o_done[t], (done - 1) & 1)) return false;
         tc::tmem_fence_after();
         const float f = move ? ex2(m - top) : 1.f;
         l *= f;
@@ -402,7 +404,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       }
       there = __all_sync(kFull, ready);
       ++done;
-      last = i;
       i = next;
       k0 = k0_next;
     }

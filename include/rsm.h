@@ -364,8 +364,10 @@ RSM_API rsm_status rsm_window_backward(const rsm_window_backward_args* args, voi
  *   cu_q              [B + 1] int32, starting at 0 and not falling;  kv_len [B] int32
  * These three are read on the device and never trusted with an address: an offset outside [0, N] is
  * clamped; a page outside the cache and places past the table's end are left out (not written, not
- * seen) and reported as RSM_ERR_BAD_PAGE by rsm_get_device_status. Places below zero are not
- * written, and a new token at one sees nothing. Rows of o (and lse) behind cu_q[B] keep their bits.
+ * seen) and reported as RSM_ERR_BAD_PAGE by rsm_get_device_status. Pages of which no place is written
+ * (or, in rsm_paged_forward, seen) are not looked up: behind a window their entries may be anything. Places
+ * below zero are not written, and a new token at one sees nothing. Rows of o (and lse) behind cu_q[B] keep
+ * their bits.
  *
  * rsm_paged_append -- writes the new tokens' k and v [N,Hkv,D] to their places. Two tokens must
  * not share a place (a page in two sequences' tables is fine while neither writes to it).
@@ -393,8 +395,9 @@ RSM_API rsm_status rsm_paged_append(const rsm_paged_append_args* args, void* str
  *   q    [N,H,D] in dtype;  o [N,H,D] in dtype;  lse [N,H] fp32 or NULL
  *   max_q  no sequence has more new tokens than this (tokens past it are not computed: their rows
  *          keep their bits). With max_q = 1 this is the single-token generation step.
- *   A row that sees nothing gets o = 0 and lse = -infinity. What the cache holds behind kv_len[b]
- *   does not matter (it may be NaN); what it holds in front of it must be finite.
+ *   A row that sees nothing gets o = 0 and lse = -infinity. What the cache holds at places that no
+ *   computed token of the sequence sees (behind kv_len[b], or hidden by the window) does not matter (it
+ *   may be NaN); what it holds at the others must be finite.
  *   workspace: at least rsm_paged_workspace_size(args) bytes (256-byte aligned; may be NULL when
  *     that is 0): partial results of long caches that several blocks share.
  *   Sizes as rsm_window_forward; page_size >= 1, N*H and max_q*H < 2^31, table_width*page_size < 2^31.

@@ -47,6 +47,21 @@ RSM_DEV Seq sequence(const AttnParams& p, int b) {
   return s;
 }
 
+// The keys that some place of [p0, p1] sees: [0, sinks) and [lo, end). A paged kernel takes the places of all its
+// sequence's rows, and neither looks up nor reads another key, though it share a tile with a seen one: behind the
+// window a cache may have given its pages back.
+struct Seen {
+  int sinks, lo, end;
+  RSM_DEV bool has(int key) const { return key < end && (key >= lo || key < sinks); }
+  // any, or all, of the n keys from k0 on
+  RSM_DEV bool any(int k0, int n) const { return k0 < end && (k0 + n > lo || k0 < sinks); }
+  RSM_DEV bool all(int k0, int n) const { return k0 + n <= end && (k0 >= lo || k0 + n <= sinks); }
+};
+
+RSM_DEV Seen keys_seen(int p0, int p1, int kv, int window, int sinks) {
+  return {sinks, window > 0 && p0 >= window ? p0 - window + 1 : 0, min(p1 + 1, kv)};
+}
+
 // The key tiles that places [p0, p1] may see (p1 >= p0), as a walk over n tiles: the first `ns`
 // are tiles 0..ns-1 (sinks), the others follow from tile `first`.
 struct Walk {
@@ -56,13 +71,12 @@ struct Walk {
 
 RSM_DEV Walk key_walk(int p0, int p1, int kv, int window, int sinks, int bn) {
   Walk w;
-  const int end = min(p1 + 1, kv);  // keys [0, end)
-  if (end <= 0) return {0, 0, 0};
-  const int last = (end - 1) / bn;
-  const int lo = window > 0 && p0 >= window ? p0 - window + 1 : 0;
-  const int s = min(sinks, end);
+  const Seen seen = keys_seen(p0, p1, kv, window, sinks);
+  if (seen.end <= 0) return {0, 0, 0};
+  const int last = (seen.end - 1) / bn;
+  const int s = min(sinks, seen.end);
   w.ns = s > 0 ? (s - 1) / bn + 1 : 0;
-  w.first = max(w.ns, lo / bn);
+  w.first = max(w.ns, seen.lo / bn);
   w.n = w.ns + max(0, last - w.first + 1);
   return w;
 }

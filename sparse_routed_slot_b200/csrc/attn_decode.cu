@@ -126,6 +126,7 @@ __global__ void __launch_bounds__(Layout<DP>::kThreads, 2) attn_decode_kernel(co
 
   const Walk walk = key_walk(s.pos0, s.pos0 + nq - 1, s.kv, p.window, p.sinks, kKeys);
   const int w0 = (int)((int64_t)walk.n * split / p.splits), w1 = (int)((int64_t)walk.n * (split + 1) / p.splits);
+  const Seen seen = keys_seen(s.pos0, s.pos0 + nq - 1, s.kv, p.window, p.sinks);
   const float scale2 = p.scale * kLog2e;
   const int64_t row_step = (int64_t)p.Hkv * D;
   const bool known = ONE || p.page % 8 == 0;  // where a tile's halves start is looked up ahead
@@ -140,13 +141,13 @@ __global__ void __launch_bounds__(Layout<DP>::kThreads, 2) attn_decode_kernel(co
 #pragma unroll
     for (int j = 0; j < kB * 4; ++j) o[n][j][0] = o[n][j][1] = o[n][j][2] = o[n][j][3] = 0.f;
   }
-  // Where a tile of keys, or each half of it, starts; -1 where there is no such key or page.
+  // Where a tile of keys, or each half of it, starts; -1 where it has no key that is seen, or no page.
   struct Base {
     int64_t part[ONE ? 1 : 2];
   };
-  // Offset of key k0 + i of a tile; -1 where there is no such key.
+  // Offset of key k0 + i of a tile; -1 where nothing sees it or it has no page.
   auto offset = [&](int k0, int i, const Base& base) -> int64_t {
-    if (k0 + i >= s.kv) return -1;
+    if (!seen.has(k0 + i)) return -1;
     if (!known) return kv_offset(p, b, hk, k0 + i);
     const int64_t from = base.part[ONE || i < 8 ? 0 : 1];
     return from < 0 ? -1 : from + (ONE ? i : i & 7) * row_step;
@@ -156,7 +157,7 @@ __global__ void __launch_bounds__(Layout<DP>::kThreads, 2) attn_decode_kernel(co
     const int k0 = w < w1 ? walk.tile(w) * kKeys : 0;
 #pragma unroll
     for (int h = 0; h < (ONE ? 1 : 2); ++h)
-      base.part[h] = known && w < w1 && k0 + 8 * h < s.kv ? kv_offset(p, b, hk, k0 + 8 * h) : -1;
+      base.part[h] = known && w < w1 && seen.any(k0 + 8 * h, ONE ? kKeys : 8) ? kv_offset(p, b, hk, k0 + 8 * h) : -1;
     return base;
   };
   auto held = [&](const Base& base) { return base.part[0] >= 0 && (ONE || base.part[ONE ? 0 : 1] >= 0); };
@@ -176,7 +177,7 @@ __global__ void __launch_bounds__(Layout<DP>::kThreads, 2) attn_decode_kernel(co
   auto fetch = [&](int w, const Base& base, int stage) {
     const uint32_t to = ring + stage * 2 * L::kTile;
     const int k0 = walk.tile(w) * kKeys;
-    if (full_rows && w < w1 && held(base) && k0 + kKeys <= s.kv) {
+    if (full_rows && w < w1 && held(base) && seen.all(k0, kKeys)) {
       const __nv_bfloat16 *fk = lane_k + base.part[0], *fv = lane_v + base.part[0];
 #pragma unroll
       for (int i = 0; i < kKeys * kPieces / 32; ++i) {

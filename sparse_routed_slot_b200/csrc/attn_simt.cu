@@ -178,6 +178,7 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const AttnParams p,
   const Walk walk = key_walk(s.pos0 + r0 / G, s.pos0 + (r0 + rows - 1) / G, s.kv, p.window, p.sinks, BB);
   const int w0 = (int)((int64_t)walk.n * split / p.splits), w1 = (int)((int64_t)walk.n * (split + 1) / p.splits);
 
+  const Seen seen = keys_seen(s.pos0, s.pos0 + nq - 1, s.kv, p.window, p.sinks);
   const float scale2 = p.scale * kLog2e;
   float m[4], l[4];
   float4 acc[4][DP / 64];
@@ -191,8 +192,8 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const AttnParams p,
   for (int w = w0; w < w1; ++w) {
     const int k0 = walk.tile(w) * BB;
     __syncthreads();
-    // rows behind the last key are zero, so that a weight of zero meets no stale NaN
-    auto off = [&](int r) { return k0 + r < s.kv ? kv_offset(p, b, hk, k0 + r) : (int64_t)-1; };
+    // rows that nothing sees are zero, so that a weight of zero meets no stale NaN
+    auto off = [&](int r) { return seen.has(k0 + r) ? kv_offset(p, b, hk, k0 + r) : (int64_t)-1; };
     load_rows<T, DP, BB>(sK, p.k, D, tx, ty, off, used);
     load_rows<T, DP, BB>(sV, p.v, D, tx, ty, off);
     __syncthreads();
@@ -204,8 +205,7 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const AttnParams p,
 #pragma unroll
       for (int j = 0; j < BB / 16; ++j) {
         const int key = k0 + tx + 16 * j;
-        const bool seen = used[tx + 16 * j] && sees(pos[i], key, p.window, p.sinks);
-        if (!seen) c[i][j] = kNegInf;
+        if (!used[tx + 16 * j] || !sees(pos[i], key, p.window, p.sinks)) c[i][j] = kNegInf;
         top = fmaxf(top, c[i][j]);
       }
       const float mn = fmaxf(m[i], half_warp_max(top));

@@ -32,8 +32,8 @@
 // of tiles 0 and 1 (a wait in one does not hold the other's products back).
 // TMEM columns: S (and P) buffers of tile t at 128 t and 128 t + 64, O at 256 + t DP.
 // A paged cache is read page by page (page sizes that divide 64 or are multiples of it, from 8 on): a
-// tile is 64 / page copies. Rows of V behind the last key are cleared before P multiplies them, so what
-// the cache holds there does not matter.
+// tile is 64 / page copies, of the pages that hold a key some row of the sequence sees. Rows of V that none sees
+// are cleared before P multiplies them, so what the cache holds there does not matter.
 #include <cuda.h>
 
 #include <algorithm>
@@ -116,6 +116,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
   const Walk walk = key_walk(pos0, pos0 + ntok0 + ntok1 - 1, s.kv, p.window, p.sinks, kBN);
   const int w0 = (int)((int64_t)walk.n * split / p.splits), w1 = (int)((int64_t)walk.n * (split + 1) / p.splits);
   const int n = w1 - w0;
+  const Seen seen = keys_seen(s.pos0, s.pos0 + nq - 1, s.kv, p.window, p.sinks);
   const int ntiles = ntok1 > 0 ? 2 : 1;  // query tiles
   unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -171,7 +172,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       wanted[0] = c < n ? 1 : 0;
       if (PAGED && c < n) {
         const int key = walk.tile(w0 + c) * kBN + lane * rows;
-        const bool in = lane * rows < kBN && key < s.kv;
+        const bool in = lane * rows < kBN && seen.any(key, rows);
         if (in) page_id[0] = p.table[(int64_t)b * p.table_width + key / p.page];
         const bool usable = in && (unsigned)page_id[0] < (unsigned)p.num_pages;
         wanted[0] = __ballot_sync(kFull, usable);
@@ -307,9 +308,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
           for (int e = 0; e < 32; ++e)
             if (!(w & (1u << e))) x[c + e] = kNegInf;
         }
-        if (PAGED && (k0 + kBN > s.kv || bad)) {
-          // key r of the tile: its V row is cleared where there is no such key
-          if (r < kBN && (k0 + r >= s.kv || ((bad >> (r / 8)) & 1))) {
+        // (a tile with a key that no row of the sequence sees is whole for none)
+        if (PAGED && (bad || !seen.all(k0, kBN))) {
+          // key r of the tile: its V row is cleared where there is no such key, or nothing sees it
+          if (r < kBN && (!seen.has(k0 + r) || ((bad >> (r / 8)) & 1))) {
             unsigned char* v = sm + L::kOffV + ((i + 2) % NS) * L::kTile + r * 128;
 #pragma unroll
             for (int c = 0; c < kBlocks; ++c)

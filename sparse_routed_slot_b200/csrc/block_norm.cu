@@ -7,6 +7,8 @@
 //   dH = dh + r2 e - h r2^3 mean(e h),  dres = dH,  du = scale dH
 //   dg = du n act'(g),  f = du act(g) w_post,  dy = r1 f - y r1^3 mean(f y)
 //   dw_post = sum_rows du act(g) y r1,  dw_pre = sum_rows dx h r2
+// The cubes are never formed: h r2 and mean(e h) r2 are of the order of 1 and of e, where r2^3 is infinite for a
+// row of zeros from eps = 1e-26 down.
 // Everything is fp32, two values per instruction, between the loads and the stores; h is normalised before it
 // is rounded, and the backward forms it again from its inputs, so no rounded value enters a sum.
 //
@@ -373,7 +375,7 @@ __global__ void __launch_bounds__(THREADS, Ring<TY, T, VEC, ITER, THREADS, true>
     float two[2] = {acc.x + acc.y, acc2.x + acc2.y};
     row_sum<THREADS>(two, tpr, &buf[1][0]);
     const float rs2 = rsqrtf(two[0] * inv_d + a.eps);
-    const float2 r2 = both(rs2), k2 = both(-rs2 * rs2 * rs2 * (two[1] * inv_d)), al = both(a.scale);
+    const float2 r2 = both(rs2), k2 = both(-rs2 * (rs2 * (two[1] * inv_d))), al = both(a.scale);
     acc = both(0.f);
 #pragma unroll
     for (int i = 0; i < ITER; ++i) {
@@ -385,9 +387,9 @@ __global__ void __launch_bounds__(THREADS, Ring<TY, T, VEC, ITER, THREADS, true>
       for (int j = 0; j < VEC / 2; ++j) {
         float2 act, slope;
         activation<GATE>(g[j], act, slope);
-        const float2 dx = dxx[j], y = yy[j];
-        s2[i][j] = fma2(mul2(dx, h[i][j]), r2, s2[i][j]);
-        dH[j] = fma2(h[i][j], k2, fma2(mul2(dx, w2[i][j]), r2, dh[j]));
+        const float2 dx = dxx[j], y = yy[j], hn = mul2(h[i][j], r2);
+        s2[i][j] = fma2(dx, hn, s2[i][j]);
+        dH[j] = fma2(hn, k2, fma2(mul2(dx, w2[i][j]), r2, dh[j]));
         const float2 du = mul2(dH[j], al), ya = mul2(y, r1), dn = mul2(du, act);
         if (GATE != kNoGate) dg[j] = mul2(mul2(du, slope), mul2(ya, w1[i][j]));
         s1[i][j] = fma2(dn, ya, s1[i][j]);
@@ -401,14 +403,14 @@ __global__ void __launch_bounds__(THREADS, Ring<TY, T, VEC, ITER, THREADS, true>
     }
     one[0] = acc.x + acc.y;
     row_sum<THREADS>(one, tpr, &buf[0][1]);
-    const float2 k1 = both(-rs1 * rs1 * rs1 * (one[0] * inv_d));
+    const float2 k1 = both(-rs1 * (rs1 * (one[0] * inv_d)));
     if (a.dy) {
 #pragma unroll
       for (int i = 0; i < ITER; ++i) {
         const int c = (t + i * tpr) * VEC;
         const Raw<TY, VEC> y = R::y(in, i);
 #pragma unroll
-        for (int j = 0; j < VEC / 2; ++j) h[i][j] = fma2(y[j], k1, mul2(h[i][j], r1));
+        for (int j = 0; j < VEC / 2; ++j) h[i][j] = fma2(mul2(y[j], r1), k1, mul2(h[i][j], r1));
         if (live && c < a.d) store_vec<TY, VEC>(static_cast<TY*>(a.dy) + base + c, h[i]);
       }
     }

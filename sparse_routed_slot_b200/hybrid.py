@@ -89,8 +89,8 @@ def _scale(scale, D):
 
 
 def _int(x):
-    """A C int; past its range the largest one, which is as good as no limit."""
-    return min(int(x), _INT_MAX)
+    """A C int; past its range the largest one, which is as good as no limit, or one below zero, which is refused."""
+    return max(min(int(x), _INT_MAX), -_INT_MAX)
 
 
 # ------------------------------------------------------------------------------ window attention

@@ -61,7 +61,14 @@ def _first(t, name, dims):
         raise ValueError(f"{name} must be a CUDA tensor")
     if dims and t.dim() != len(dims):
         raise ValueError(f"{name} must be [{','.join(dims)}], got {tuple(t.shape)}")
+    _ints(t, name)
     return t.dtype, t.shape, t.get_device()
+
+
+def _ints(t, name):
+    """Refuses sizes that are no C ints (the library takes them as such)."""
+    if t.numel() > _INT_MAX and max(t.shape) > _INT_MAX:
+        raise ValueError(f"{name} has a size of 2^31 or more: {tuple(t.shape)}")
 
 
 def _run(fn, args, index, size_fn=None, workspace=None):
@@ -199,6 +206,7 @@ def paged_append(k, v, k_cache, v_cache, page_table, cu_q, kv_len) -> None:
 def _table(page_table):
     if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
         raise ValueError("page_table must be a CUDA tensor [B, width]")
+    _ints(page_table, "page_table")
     return page_table.shape
 
 

@@ -59,3 +59,25 @@ def test_far_negatives_are_refused(rsm, x):
         for kw in (dict(window=x), dict(window=3, sinks=x), dict(max_q=x)):
             with pytest.raises(rsm.RSMError, match="INVALID"):
                 rsm.paged_forward(**{**paged(), **kw})
+
+
+@pytest.mark.parametrize("n", [2**31, 2**32 + 5, 2**32 + 64])
+def test_sizes_past_a_c_int_are_refused(rsm, n):
+    """2^32 + 5 tokens would be taken for 5."""
+    with FakeTensorMode():
+        for kw in (paged(N=n, H=1, Hkv=1, D=8), paged(pages=n, page=1, Hkv=1, D=8), paged(pages=1, page=n, Hkv=1, D=8),
+                   paged(B=1, width=n)):
+            with pytest.raises(ValueError, match="2\\^31"):
+                rsm.paged_forward(**kw)
+            places = {x: kw[x] for x in ("k_cache", "v_cache", "page_table", "cu_q", "kv_len")}
+            k = fake(kw["q"].shape[0], *kw["k_cache"].shape[2:])
+            with pytest.raises(ValueError, match="2\\^31"):
+                rsm.paged_append(k, k, **places)
+        x = fake(1, n, 1, 8)
+        with pytest.raises(ValueError, match="2\\^31"):
+            rsm.window_forward(x, x, x, 3)
+        x, w = fake(1, n), fake(n, dtype=torch.float32)
+        with pytest.raises(ValueError, match="2\\^31"):
+            rsm.block_norm_forward(x, None, x, w)
+        with pytest.raises(ValueError, match="2\\^31"):
+            rsm.block_norm_backward(x, None, x, w, dh=x)

@@ -242,6 +242,15 @@ def backward(q, k, v, logits, f, K: int, dO=None, dHT=None, H0=None, *, validate
     return out
 
 
+def gradient(g):
+    """An output's gradient as the library takes it: contiguous and on a 16-byte boundary. Autograd promises neither
+    (a part of a concatenation gets a slice of its gradient)."""
+    if g is None:
+        return None
+    g = g.contiguous()
+    return g if g.data_ptr() % 16 == 0 else g.clone()
+
+
 class RSMFunction(torch.autograd.Function):
     """The mixer as an autograd function: forward runs rsm_forward, backward runs rsm_backward.
     Inputs q, k, v, logits, f (and optionally H0); outputs o and H_T."""
@@ -257,8 +266,8 @@ class RSMFunction(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dO, dHT):
         q, k, v, logits, f, H0 = ctx.saved_tensors
-        g = backward(q, k, v, logits, f, ctx.K, None if dO is None else dO.float().contiguous(),
-                     None if dHT is None else dHT.float().contiguous(), H0 if ctx.has_h0 else None)
+        g = backward(q, k, v, logits, f, ctx.K, gradient(None if dO is None else dO.float()),
+                     gradient(None if dHT is None else dHT.float()), H0 if ctx.has_h0 else None)
         cast = lambda t, like: t.to(like.dtype)
         return (cast(g["dq"], q), cast(g["dk"], k), cast(g["dv"], v), g["dlogits"], g["df"], None,
                 g["dH0"] if ctx.has_h0 else None)

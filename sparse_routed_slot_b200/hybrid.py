@@ -13,7 +13,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _lib
-from .api import _DTYPES
+from .api import _DTYPES, gradient
 
 _NO_SIZE = ctypes.c_size_t(-1).value
 _ACTS = {"silu": _lib.RSM_ACT_SILU, "sigmoid": _lib.RSM_ACT_SIGMOID}
@@ -179,7 +179,7 @@ class WindowFunction(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dO):
         q, k, v, o, lse, low = ctx.saved_tensors
-        g = window_backward(q, k, v, o, lse, dO.contiguous(), *ctx.how, low=low, need=ctx.needs_input_grad[:3])
+        g = window_backward(q, k, v, o, lse, gradient(dO), *ctx.how, low=low, need=ctx.needs_input_grad[:3])
         return g["dq"], g["dk"], g["dv"], None, None, None
 
 
@@ -323,6 +323,5 @@ class BlockNormFunction(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, dh, dx):
-        g = block_norm_backward(*ctx.saved_tensors, dh=None if dh is None else dh.contiguous(),
-                                dx=None if dx is None else dx.contiguous(), need=ctx.needs_input_grad[:5], **ctx.how)
+        g = block_norm_backward(*ctx.saved_tensors, dh=gradient(dh), dx=gradient(dx), need=ctx.needs_input_grad[:5], **ctx.how)
         return g["dy"], g["dgate"], g["dresidual"], g["dw_post"], g["dw_pre"], None, None, None

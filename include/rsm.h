@@ -54,8 +54,8 @@ typedef enum rsm_status {
   RSM_ERR_INVALID_ARG = 1,  /* null pointer where one is required, bad size, misalignment */
   RSM_ERR_UNSUPPORTED = 2,  /* valid arguments outside the sizes this build implements */
   RSM_ERR_CUDA = 3,         /* a CUDA call or launch failed; see rsm_last_error() */
-  RSM_ERR_NONFINITE = 4,    /* RSM_FLAG_VALIDATE found a non-finite logit or a non-finite/positive f */
-  RSM_ERR_WORKSPACE = 5,    /* workspace missing or smaller than rsm_forward_workspace_size() */
+  RSM_ERR_NONFINITE = 4,    /* RSM_FLAG_VALIDATE found a non-finite input, or f > 0 */
+  RSM_ERR_WORKSPACE = 5,    /* workspace missing or smaller than the call's ..._workspace_size() */
   RSM_ERR_TIMEOUT = 6,      /* a bounded device wait gave up (reported by rsm_get_device_status) */
   RSM_ERR_BAD_PAGE = 7      /* a page table or length outside the cache (reported by rsm_get_device_status) */
 } rsm_status;
@@ -85,7 +85,8 @@ typedef enum rsm_router {
 } rsm_router;
 
 enum {
-  /* Device-side check of the preconditions: a non-finite logit or a non-finite or positive f is
+  /* Device-side check of the preconditions: a non-finite logit, a non-finite or positive f, or (in the
+   * attention calls) a non-finite q, k, v or dO is
    * reported as RSM_ERR_NONFINITE by rsm_get_device_status (results are then undefined). */
   RSM_FLAG_VALIDATE = 1,
   /* Testing aid for the bounded-wait error paths (no counterpart on the pages; never set in normal
@@ -298,6 +299,8 @@ RSM_API rsm_status rsm_backward(const rsm_backward_args* args, void* stream);
  *   Supported: 8 <= D <= 256 with D % 8 == 0, Hkv dividing H with H / Hkv <= 64, window >= 1,
  *   sinks >= 0, scale > 0 and finite, T*H < 2^31. B, T or H may be 0 (nothing is launched). Outputs
  *   must not alias inputs or one another.
+ *   bf16 with D <= 128 runs on the tensor cores; a larger D, and fp32, on CUDA cores in fp32, at about a
+ *   seventeenth of that rate (8 x 2048 tokens, window 512: 4 heads of 256 take 1493 us, 8 of 128 take 88).
  * ------------------------------------------------------------------------------------------- */
 typedef struct rsm_window_args {
   int B, T, H, Hkv, D;
@@ -401,6 +404,9 @@ RSM_API rsm_status rsm_paged_append(const rsm_paged_append_args* args, void* str
  *   workspace: at least rsm_paged_workspace_size(args) bytes (256-byte aligned; may be NULL when
  *     that is 0): partial results of long caches that several blocks share.
  *   Sizes as rsm_window_forward; page_size >= 1, N*H and max_q*H < 2^31, table_width*page_size < 2^31.
+ *   Fast in bf16: any D and page_size while max_q * H / Hkv <= 16; more rows with D <= 128 and a
+ *   page_size of 8, 16, 32 or a multiple of 64. Chunks over other pages or heads, and fp32, run on CUDA
+ *   cores (4 x 512 tokens over 8192 keys, 16/4 heads of 128: 147 us with pages of 64, 7.7 ms with 24).
  *   Outputs must not alias inputs or one another.
  * ------------------------------------------------------------------------------------------- */
 typedef struct rsm_paged_args {

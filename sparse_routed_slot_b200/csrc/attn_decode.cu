@@ -15,6 +15,8 @@
 //                 2 t + 8, 2 t + 9; byte permutes make the pairs of keys that the product takes, and column
 //                 8 g + 2 j (+ 1) stands in row g (g + 8) of product j
 //   P^T from S^T's accumulators by an 8 x 8 transpose across the lanes.
+// With 9 to 16 rows of head dimension 256 the registers do not suffice (450 to 640 bytes spilled per thread): 64
+// sequences of 4096 keys, 4 key/value heads, take 282 us there (3.8 TB/s), with up to 8 rows 170 to 174 (6.2 to 6.3).
 // The weights are rounded to bf16 for the product; scores, statistics and sums are fp32. As in the tile
 // kernel, the reference of a row's exponentials moves only past 2^32. The block's warps join at the end in
 // shared memory. Up to 8 blocks that share a sequence's keys are a cluster and join through each other's

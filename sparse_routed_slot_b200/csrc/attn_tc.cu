@@ -24,8 +24,9 @@
 // 2100). The two warps of a scheduler, one of each query tile, take turns at their exponentials: left
 // alone they fall into step, and the special function units idle while both load and look for maxima.
 // A step of 64 keys and two query tiles needs 1024 cycles of the special function units and 1280 of the
-// tensor core (S of 64 keys runs at 3/4 rate, bound by its operands from shared memory) and takes 1750 (before
-// the rounded weights were summed as well).
+// tensor core (S of 64 keys runs at 3/4 rate, bound by its operands from shared memory) and takes 1950 (32768
+// tokens, 16/4 heads of 128: from windows of 1024, 4096 and 8192 keys). A block takes 8000 to 10000 besides, to
+// start, to drain and to write: one block per SM hides none of it.
 // K and V tiles serve both query tiles.
 //
 // Warps: 0-3 and 4-7 the rows of tiles 0 and 1 (a thread per row), 8 copies (TMA), 9 and 10 the MMA issuers

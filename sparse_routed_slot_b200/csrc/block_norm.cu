@@ -19,9 +19,9 @@
 //
 // 2^25 values, us, forward / gradients (the copy rate: 51 / 82 bf16, 61 / 102 with fp32 y, 102 / 164 fp32):
 //   d           64         128        1024       2048       2500         4096       8192
-//   bf16        61 / 114   61 / 118   59 / 124   60 / 138    -  / 200    65 / 120   64 / 130
-//   fp32 y      75 / 144   75 / 146   70 / 163   72 / 161    -  / 198    78 / 144    -  / 163
-//   fp32       115 / 190  115 / 189  117 / 179  119 / 179    -  / 253   114 / 177  117 / 193
+//   bf16        59 / 110   59 / 115   55 / 121   58 / 133  105 / 197    58 / 115   60 / 127
+//   fp32 y      71 / 138   71 / 144   66 / 165   65 / 162  109 / 196    71 / 146   66 / 172
+//   fp32       114 / 198  114 / 198  116 / 182  122 / 180  132 / 264   119 / 179  121 / 194
 // What is left is the chain of three row sums in the gradients (two in the forward) and, where d is not a
 // multiple of 8, bf16 pieces of 8 bytes. With the next row in registers instead of the ring (and 256 threads or
 // more, a power of two, per block) the gradients of bf16 took 318, 173, 163, 173, 308, 190 and 235.

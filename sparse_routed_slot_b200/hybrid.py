@@ -223,7 +223,8 @@ def paged_forward(q, k_cache, v_cache, page_table, cu_q, kv_len, max_q: int, *, 
     sees every earlier place, else the last `window` and the first `sinks`.
 
     Returns dict(o [N,H,D] in q's dtype, lse [N,H] fp32 or None); a row that sees nothing gets zeros.
-    device_status() reports pages and lengths outside the cache."""
+    device_status() reports pages and lengths outside the cache. Pages that nothing sees are not looked up:
+    behind a window they may have been given back."""
     dtype, shape, index = _first(q, "q", "NHD")
     cshape = _first(k_cache, "k_cache", _CACHE)[1]
     pages, page, Hkv, D = cshape

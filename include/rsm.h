@@ -403,7 +403,8 @@ RSM_API rsm_status rsm_paged_append(const rsm_paged_append_args* args, void* str
  *   may be NaN); what it holds at the others must be finite.
  *   workspace: at least rsm_paged_workspace_size(args) bytes (256-byte aligned; may be NULL when
  *     that is 0): partial results of long caches that several blocks share.
- *   Sizes as rsm_window_forward; page_size >= 1, N*H and max_q*H < 2^31, table_width*page_size < 2^31.
+ *   Sizes as rsm_window_forward; page_size >= 1, N*H and max_q*H < 2^31, table_width*page_size <=
+ *   2^31 - 256.
  *   Fast in bf16: any D and page_size while max_q * H / Hkv <= 16; more rows with D <= 128 and a
  *   page_size of 8, 16, 32 or a multiple of 64. Chunks over other pages or heads, and fp32, run on CUDA
  *   cores (4 x 512 tokens over 8192 keys, 16/4 heads of 128: 147 us with pages of 64, 7.7 ms with 24).

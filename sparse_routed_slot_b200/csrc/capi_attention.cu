@@ -143,8 +143,9 @@ rsm_status check_cache(int B, int N, int Hkv, int D, int num_pages, int page_siz
   if (B < 0 || N < 0) return fail(RSM_ERR_INVALID_ARG, "B and N must be >= 0");
   if (num_pages < 0 || table_width < 0) return fail(RSM_ERR_INVALID_ARG, "num_pages and table_width must be >= 0");
   if (page_size < 1) return fail(RSM_ERR_INVALID_ARG, "page_size must be >= 1 (got %d)", page_size);
-  if ((int64_t)table_width * page_size > 0x7fffffff)
-    return fail(RSM_ERR_UNSUPPORTED, "table_width * page_size must stay under 2^31");
+  // (the kernels add up to a tile to a place)
+  if ((int64_t)table_width * page_size > 0x7fffff00)
+    return fail(RSM_ERR_UNSUPPORTED, "table_width * page_size must not exceed 2^31 - 256");
   return RSM_OK;
 }
 

@@ -81,3 +81,15 @@ def test_sizes_past_a_c_int_are_refused(rsm, n):
             rsm.block_norm_forward(x, None, x, w)
         with pytest.raises(ValueError, match="2\\^31"):
             rsm.block_norm_backward(x, None, x, w, dh=x)
+
+
+@pytest.mark.parametrize("page", [1, 16, 64])
+def test_places_close_to_2_31_are_refused(rsm, page):
+    """A tile that starts below 2^31 and ends past it: its end would be negative, and all of it in sight."""
+    with FakeTensorMode():
+        for places in (2**31 - 64, 2**31 - 256 + page):
+            kw = paged(B=1, page=page, width=places // page)
+            with pytest.raises(rsm.RSMError, match="UNSUPPORTED"):
+                rsm.paged_forward(**kw)
+        with pytest.raises(rsm.RSMError, match="must not be NULL"):  # the next check
+            rsm.paged_forward(**paged(B=1, page=page, width=(2**31 - 256) // page))
